@@ -109,6 +109,12 @@ __host__ __device__ inline void token_range(int K, int Kg, int lvl, bool has_lvl
 struct KeySpan {
   int lo, hi;
 };
+// The union of windows [lo, hi) of a request with K keys.  An empty one begins behind the request's
+// last 64-key group: what lies between the sinks and the window may have been given up, so it must
+// not be looked up for tokens that see sinks only.
+__host__ __device__ __forceinline__ KeySpan key_span(int lo, int hi, int K) {
+  return {lo < hi ? lo : cdiv(K, kKeyGroup) * kKeyGroup, hi};
+}
 
 // Tiles of a piece of work: tile v holds the 64-key groups 4 v .. 4 v + 3 of its axis.  Without a
 // window the axis is the sequence.  With one, the groups between the last that holds a sink

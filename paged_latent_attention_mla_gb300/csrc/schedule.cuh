@@ -44,7 +44,8 @@ __device__ __forceinline__ void token_keys(const DecodeParams& p, int b, int t, 
   token_range(K, Kg, lvl, has_lvl, p.Sq, t, p.causal, p.window_left, p.cp_world, p.cp_rank, p.cp_interleave, lo, hi);
 }
 
-// union of the visible keys of tokens [t0, t1] of request b with local bounds (arbitrary per token)
+// union of the visible keys of tokens [t0, t1] of request b with local bounds (arbitrary per token);
+// INT_MAX for the lower end where no token has a key in its window
 static __device__ __noinline__ int2 tokens_span_lvl(const DecodeParams& p, int b, int t0, int t1, int K, int Kg) {
   int lo_min = INT_MAX, hi_max = 0;
   for (int t = t0; t <= t1; ++t) {
@@ -54,7 +55,7 @@ static __device__ __noinline__ int2 tokens_span_lvl(const DecodeParams& p, int b
     // a token with nothing in its window still sees the sinks below its bound
     if (hi > lo || p.sinks > 0) hi_max = hi > hi_max ? hi : hi_max;
   }
-  return make_int2(lo_min < hi_max ? lo_min : hi_max, hi_max);
+  return make_int2(lo_min, hi_max);
 }
 
 // Union of the visible keys of tokens [t0, t1] of request b.  Without local bounds both ends of
@@ -65,12 +66,12 @@ static __device__ __noinline__ int2 tokens_span_lvl(const DecodeParams& p, int b
 __device__ __forceinline__ KeySpan tokens_span(const DecodeParams& p, int b, int t0, int t1, int K, int Kg) {
   if (p.local_visible_lens) {
     const int2 r = tokens_span_lvl(p, b, t0, t1, K, Kg);
-    return {r.x, r.y};
+    return key_span(r.x, r.y, K);
   }
   int lo0, hi0, lo1, hi1;
   token_range(K, Kg, 0, false, p.Sq, t0, p.causal, p.window_left, p.cp_world, p.cp_rank, p.cp_interleave, lo0, hi0);
   token_range(K, Kg, 0, false, p.Sq, t1, p.causal, p.window_left, p.cp_world, p.cp_rank, p.cp_interleave, lo1, hi1);
-  return {lo0, hi1};
+  return key_span(lo0, hi1, K);
 }
 
 struct Sched {
