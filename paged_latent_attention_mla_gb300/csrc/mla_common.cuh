@@ -280,7 +280,8 @@ struct RowInfo {
 
 // One piece of work of a cluster.  The work row (< 2^14) and the partial slot + 1 (0: the
 // row's only piece, written to the output) share one word; K is the request's local key
-// count, so the roles start a piece without reading seq_lens.
+// count, or the sub-band's last visible key + 1 with local bounds, so the roles start a piece
+// without reading seq_lens.
 struct Segment {
   uint32_t row_slot;   // row | (slot + 1) << 14
   int32_t tile_begin;  // tiles [tile_begin, tile_end) of the work row

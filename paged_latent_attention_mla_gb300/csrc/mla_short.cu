@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_decode(const __grid_co
   const int K = clamp_len(p, b, rank == 0 && tid == 0 ? &M.err : nullptr), Kg = global_len(p, b, K);
   const KeySpan span = tokens_span(p, b, flat0 / p.H, (min(rows_q, flat0 + kRows) - 1) / p.H, K, Kg);
   const Groups g = key_groups(span, p.sinks);
+  const int Kv = min(K, span.hi);  // slots and pages from here on no row of the tile sees
   const int per = (g.n + C - 1) / C;
   const int v0 = min(g.n, rank * per), v1 = min(g.n, v0 + per), n = v1 - v0;
   const int parts = per > 0 ? (g.n + per - 1) / per : 0;  // CTAs of the cluster with groups
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_decode(const __grid_co
     if (i >= n || lane >= nb) return;
     bool miss;
     box_page<true>(p.page_table, p.pt_stride, p.num_pages, p.page_shift, b, g.at(v0 + i) * kKeyGroup + lane * br, br,
-                   span.lo, p.sinks, K, pg, rw, miss);
+                   span.lo, p.sinks, Kv, pg, rw, miss);
     bad |= miss;
   };
   auto load = [&](int i) {
@@ -249,22 +250,22 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_decode(const __grid_co
     if (i == 0) mbar_try_wait(smem_addr(&M.q_full), 0);
     mbar_try_wait(bar, (i >> 1) & 1);
     const int key0 = g.at(v0 + i) * kKeyGroup;
-    // slots past the request's length: any bits there must not reach P.c
+    // slots past the last visible key: any bits there must not reach P.c
     if constexpr (E4M3) {
       if (i == 0) {
         widen<1>(smem + kOffK, smem, 64, tid);
         __syncthreads();
       }
-      widen<RT == 4 ? 2 : 4>(smem + kOffRaw + (i & 1) * kRawBytes, smem + kOffK, K - key0, tid);  // RT 4: 4 spills
+      widen<RT == 4 ? 2 : 4>(smem + kOffRaw + (i & 1) * kRawBytes, smem + kOffK, Kv - key0, tid);  // RT 4: 4 spills
       __syncthreads();
       // the group as it landed is read: the one after next goes there
       if (warp == 0 && i + 2 < n) load(i + 2);
     } else {
       // every warp is done with the other stage: the next group goes there
       if (warp == 0 && i > 0 && i + 1 < n) load(i + 1);
-      if (key0 + kKeyGroup > K) {
+      if (key0 + kKeyGroup > Kv) {
         for (int kb = 0; kb < 8; ++kb)
-          zero_block_rows(smem + kOffK + (i & 1) * kStageBytes + kb * kBlockBytes, max(K - key0, 0), tid, kShortThreads);
+          zero_block_rows(smem + kOffK + (i & 1) * kStageBytes + kb * kBlockBytes, max(Kv - key0, 0), tid, kShortThreads);
         fence_proxy_async_smem();
         __syncthreads();
       }

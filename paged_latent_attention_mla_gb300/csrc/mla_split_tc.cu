@@ -638,7 +638,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // this thread's M row: its token's visible keys (none for a padding row)
       const int b = sg.row() / DS.Qb, flat = kTileM * (sg.row() % DS.Qb) + 64 * (int)rank + row;
       int key_lo = 0, key_hi = 0;
-      if (flat < rows_q) token_keys(p, b, flat / p.H, sg.K, global_len(p, b, sg.K), key_lo, key_hi);
+      if (flat < rows_q) {
+        // the window's floor is taken on the whole length, which sg.K is not with local bounds
+        const int Kw = WINDOW && p.local_visible_lens ? clamp_len(p, b, nullptr) : sg.K;
+        token_keys(p, b, flat / p.H, sg.K, global_len(p, b, Kw), key_lo, key_hi);
+      }
       const int n = sg.tile_end - sg.tile_begin;
       const TileAxis ax = axis_of(sg);
       float m_ref = -INFINITY, l = 0.f;

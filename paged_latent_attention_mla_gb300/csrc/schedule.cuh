@@ -81,9 +81,9 @@ struct Sched {
   int Gd;  // groups the tiles are dealt to
 };
 
-// a sub-band's tiles (the union of its work rows), its first key and its axis
+// a sub-band's tiles (the union of its work rows), its keys' ends and its axis
 struct SubSpan {
-  int tile_lo, n, key_lo;
+  int tile_lo, n, key_lo, key_hi;
   TileAxis axis;
 };
 
@@ -96,6 +96,7 @@ __device__ __forceinline__ SubSpan sub_span(const DecodeParams& p, const DealSha
   const KeySpan s = tokens_span(p, b, t0, t1, K, Kg);
   SubSpan u;
   u.key_lo = s.lo;
+  u.key_hi = s.hi;
   u.axis = tile_axis<WINDOW>(s.lo, p.sinks);
   tile_span<WINDOW>(s, u.axis, p.sinks, u.tile_lo, u.n);
   return u;
@@ -232,7 +233,9 @@ __device__ __forceinline__ int build_segments(const DecodeParams& p, const Sched
           sg.row_slot = (uint32_t)(b * d.Qb + i) | ((uint32_t)(slot + 1) << 14);
           sg.tile_begin = t_begin;
           sg.tile_end = t_end;
-          sg.K = K;
+          // past every local bound the pages are nobody's: the piece ends there (without local
+          // bounds the request's last token sees its last key)
+          sg.K = p.local_visible_lens ? min(K, sub.key_hi) : K;
           sg.parts = (uint32_t)np | ((uint32_t)(g - g_first) << 16);
           sg.key_lo = sub.key_lo;
           has = true;

@@ -61,6 +61,24 @@ def test_bounds_below_the_window_read_no_page_given_up(H, clusters, kernels, dty
     check(*run(prob, d, lvl, sinks, kernels, num_clusters=clusters), reference(prob, sinks, lvl))
 
 
+@pytest.mark.parametrize("H,clusters,kernels", KERNELS)
+@pytest.mark.parametrize("dtype,P", [("bf16", 8), ("e4m3", 16), ("bf16", 64), ("e4m3", 128)])
+@pytest.mark.parametrize("window,sinks", [(-1, 0), (900, 0), (300, 5)])
+def test_pages_past_every_bound_hold_any_bits(H, clusters, kernels, dtype, P, window, sinks):
+    """Pages below the request's length whose keys no token sees, because they lie past every bound."""
+    lvl = torch.tensor([[10, 3], [64, 64], [500, 1], [0, 1], [999, 700], [600, 990]], dtype=torch.int32)
+    prob = wl.make_problem("uniform", seed=P + window, H=H, Sq=2, causal=False, window_left=window, dtype=dtype, page_size=P,
+                           seq_lens=[1000] * len(lvl))
+    d = prob.device_inputs("cuda")
+    poisoned = 0
+    for b, bounds in enumerate(lvl.tolist()):
+        for j in range(-(-max(bounds) // P), -(-1000 // P)):
+            nan_page(prob, d, int(d["page_table"][b, j]))
+            poisoned += 1
+    assert poisoned > 0
+    check(*run(prob, d, lvl, sinks, kernels, num_clusters=clusters), reference(prob, sinks, lvl))
+
+
 @pytest.mark.parametrize("clusters", [0, 76])
 @pytest.mark.parametrize("P", [16, 64])
 def test_ranks_without_window_keys_read_no_page_given_up(clusters, P):
