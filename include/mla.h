@@ -432,8 +432,8 @@ MLA_API mla_status_t mla_cache_workspace(const mla_cache_t *cache, int rows, siz
  *  seq_lens_out [N], ref_count_out [num_pages]
  * The outputs may be the inputs' own arrays (the table and the lengths together, the counts
  * by themselves; the arrays then have room for max(B, N) rows), else they must not overlap
- * them.  B and N are 0 to 16384.  With decode context parallelism, lengths are this rank's
- * and window_left is -1.
+ * them.  B and N are 0 to 16384, N * page_table_stride below 2^31 (MLA_ERR_UNSUPPORTED
+ * otherwise).  With decode context parallelism, lengths are this rank's and window_left is -1.
  */
 MLA_API mla_status_t mla_cache_fork(const int32_t *page_table, const int32_t *seq_lens, int B, const int32_t *parents,
                                     const int32_t *new_tokens, int N, const int32_t *ref_count, void *ckv_cache,

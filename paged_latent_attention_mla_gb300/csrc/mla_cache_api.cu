@@ -2,6 +2,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstdint>
 
@@ -121,6 +122,8 @@ mla_status_t mla_cache_fork(const int32_t* page_table, const int32_t* seq_lens, 
   if (B < 0 || N < 0 || window_left < -1 || sink_tokens < 0) return MLA_ERR_INVALID_ARG;
   if (B > kMaxCacheRows || N > kMaxCacheRows || sink_tokens > (1 << 30)) return MLA_ERR_UNSUPPORTED;
   const int W = cache->page_table_stride;
+  // the pages all rows ask for, at most their tables' entries, are summed in 32 bits
+  if ((long long)N * W > INT_MAX) return MLA_ERR_UNSUPPORTED;
   if (!ints_ok(page_table, B) || !ints_ok(seq_lens, B) || !ints_ok(parents, N) || !aligned(new_tokens, 4) ||
       !ints_ok(page_table_out, N) || !ints_ok(seq_lens_out, N) || !ints_ok(ref_count, 1) || !ints_ok(ref_count_out, 1) ||
       !aligned(status, 4) || !pools_ok(ckv_cache, kpe_cache) || !workspace || !aligned(workspace, 256))

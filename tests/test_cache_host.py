@@ -297,3 +297,17 @@ def test_decode_wrapper_rejects_what_does_not_fit_its_config(lib):
     ]:
         with pytest.raises(error):
             call(**over)
+
+
+def test_fork_rejects_tables_whose_entries_pass_32_bits(lib):
+    """The pages the rows ask for are summed in 32 bits; no row asks for more than its table row holds."""
+    def status(N, stride, page_size=8, **over):
+        # arrays far apart; a workspace too small, so that what is accepted launches nothing
+        return fork_status(lib, cache=layout(stride=stride, page_size=page_size), N=N, pt=1 << 40, pto=1 << 44, wsb=256, **over)
+
+    assert status(16384, 131072) == n.MLA_ERR_UNSUPPORTED
+    assert status(16384, 131071) == n.MLA_ERR_WORKSPACE_TOO_SMALL
+    assert status(16, 1 << 27) == n.MLA_ERR_UNSUPPORTED
+    assert status(15, 1 << 27) == n.MLA_ERR_WORKSPACE_TOO_SMALL
+    assert status(2049, 1 << 20, page_size=1024) == n.MLA_ERR_UNSUPPORTED
+    assert status(1, 1 << 27, B=16384) == n.MLA_ERR_WORKSPACE_TOO_SMALL  # the present rows ask for nothing
