@@ -318,9 +318,9 @@ MLA_API const char *mla_status_string(mla_status_t status);
  *
  * The state is the caller's, all of it on the device: the pools ckv / kpe, a page table and
  * lengths as mla_decode takes them, and a reference count per page (how many rows, of this
- * table or elsewhere, hold it; a count of 0 or less is a free page).  A row of K keys holds
- * the pages of its entries [0, ceil(K / page_size)); an entry MLA_NO_PAGE there holds none
- * (given up behind a window).  The calls enqueue kernels and neither allocate nor
+ * table or elsewhere, hold it; a count of 0 or less, down to 2^14 - 2^31, is a free page).  A
+ * row of K keys holds the pages of its entries [0, ceil(K / page_size)); an entry MLA_NO_PAGE
+ * there holds none (given up behind a window).  The calls enqueue kernels and neither allocate nor
  * synchronize, so a decode loop of mla_cache_fork, mla_cache_append and mla_decode can be
  * captured into a CUDA graph.  Calls that overlap on the GPU need workspaces of their own
  * and must not write the same arrays.  Fork and compact plan on one cluster of 16 blocks: they

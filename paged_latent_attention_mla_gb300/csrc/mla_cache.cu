@@ -509,13 +509,17 @@ constexpr int kSame = 0;    // nobody else holds the last page: who writes on in
 constexpr int kClaims = 1;  // others hold it, or may: the writers claim it
 constexpr int kMixed = 2;   // some child gives keys up: counts go row by row, writers claim
 
+// A row's claim on a page, in the page's count: below every count a caller keeps.
+__device__ __forceinline__ int claim_of(int row) { return INT_MIN + row; }
+__device__ __forceinline__ bool is_claim(int count) { return count < INT_MIN + kMaxCacheRows; }
+
 // One cluster plans the whole step.  Phases, a cluster barrier between them:
 //   0  children of every input row
 //   1  counts: per input row where its children are alike (a plain decode step changes none),
 //      else +1 for every page an output row shares and -1 for every page its parent held;
 //      where nobody claims a page, which rows copy
 //   2  (only if there are claims) a page a row is about to write that nobody shares goes to the
-//      claimants' lowest row: atomicMin of row - N, negative; after one more barrier who won
+//      claimants' lowest row: atomicMin of claim_of(row); after one more barrier who won
 //   3  the fresh pages each row needs, free pages counted
 //   4  each row's place in the free list, and the list (free pages in ascending order)
 // All sums are integer sums and minima: the result does not depend on their order.
@@ -663,9 +667,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fork_plan_kernel(const __grid
   for (int c = 0; c < kPlanCtas; ++c) any_claim |= s_claims[c] != 0;
   if (any_claim) {
     const bool there = is_page(page, p.num_pages);
-    if (claims && there && __ldcg(p.ref + page) <= 0) atomicMin(p.ref + page, i - p.N);
+    if (claims && there && __ldcg(p.ref + page) <= 0) atomicMin(p.ref + page, claim_of(i));
     cluster_sync();
-    if (claims && there) copy = __ldcg(p.ref + page) != i - p.N;
+    if (claims && there) copy = __ldcg(p.ref + page) != claim_of(i);
     if (claims && !there) {
       err |= kErrBadPage;  // the page whose keys the row keeps is not there
       r.page = -1;
@@ -677,7 +681,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fork_plan_kernel(const __grid
   int w0, w1;
   my_words(p.num_pages, rank, warp, w0, w1);
   uint32_t mine;
-  int fbase = scan_words(p.ref, p.num_pages, w0, w1, words, mine, [](int v) { return v == 0; });
+  int fbase = scan_words(p.ref, p.num_pages, w0, w1, words, mine, [](int v) { return v <= 0 && !is_claim(v); });
   int off = __reduce_add_sync(0xffffffffu, need), cta_need, cta_free;
   const int before_me = off > 0 ? lane_prefix(need) : 0;
   warp_sums(off, part[0], cta_need);
