@@ -171,13 +171,23 @@ PyObject* tuple_of(std::initializer_list<at::Tensor> ts) {
   return r;
 }
 
-// a dense tensor of at least n elements of this many bytes
-void dense(const char* name, const at::Tensor& t, int64_t bytes, int64_t n) {
+// a dense tensor of at least n elements of this type (or of its bits in integers of its size)
+void dense(const char* name, const at::Tensor& t, at::ScalarType type, int64_t n) {
+  const auto dt = t.scalar_type();
+  const int64_t bytes = (int64_t)c10::elementSize(type);
   if ((int64_t)t.element_size() != bytes)
     raise(PyExc_TypeError, std::string(name) + " has elements of " + std::to_string(t.element_size()) + " bytes, expected " +
                                std::to_string(bytes));
+  if (dt != type && at::isFloatingType(dt))
+    raise(PyExc_TypeError, std::string(name) + " must be " + c10::toString(type) + ", not " + c10::toString(dt));
   if (!t.is_contiguous()) raise(PyExc_ValueError, std::string(name) + " must be contiguous");
   if (t.numel() < n) raise(PyExc_ValueError, std::string(name) + " is too small: " + shape_of(t));
+}
+
+// rows of this many entries, where more than one is read
+void row_stride(const char* name, const at::Tensor& t, int64_t rows, int64_t n) {
+  if (rows > 1 && t.dim() > 1 && t.size(-1) != n)
+    raise(PyExc_ValueError, std::string(name) + " must have rows of " + std::to_string(n) + ", not " + shape_of(t));
 }
 
 // (q_latent, q_rope, ckv, kpe, page_table, seq_lens, scale, window_left, out, lse, want_lse, workspace,
@@ -194,27 +204,36 @@ PyObject* decode(Args a) {
   if (!address) raise(PyExc_ValueError, "no config");
   mla_config_t cfg = *static_cast<const mla_config_t*>(address);
   const at::Tensor *global = a.optional("global_seq_lens"), *local = a.optional("local_visible_lens");
-  if (ql.dim() != 4 || pc.dim() != 3) raise(PyExc_ValueError, "q_latent must be [B, Sq, H, 512] and ckv [pages, page_size, 512]");
-  const int es = cfg.qkv_dtype == MLA_E4M3 ? 1 : 2;
+  if (ql.dim() != 4 || ql.size(1) != cfg.seq_len_q || ql.size(3) != 512)
+    raise(PyExc_ValueError, "q_latent must be [B, " + std::to_string(cfg.seq_len_q) + ", H, 512], not " + shape_of(ql));
+  if (pc.dim() != 3 || pc.size(2) != 512) raise(PyExc_ValueError, "ckv must be [pages, page_size, 512], not " + shape_of(pc));
+  const auto es = cfg.qkv_dtype == MLA_E4M3 ? at::kFloat8_e4m3fn : at::kBFloat16;
+  const auto os = cfg.out_dtype == MLA_F32 ? at::kFloat : at::kBFloat16;
   const int64_t B = ql.size(0), H = ql.size(2), rows = B * cfg.seq_len_q * H, keys = (int64_t)cfg.num_pages * pc.size(1);
   dense("q_latent", ql, es, rows * 512);
   dense("q_rope", qr, es, rows * 64);
   dense("ckv", pc, es, keys * 512);
   dense("kpe", pk, es, keys * 64);
-  dense("page_table", table, 4, B * cfg.page_table_stride);
-  dense("seq_lens", lens, 4, B);
-  if (out) dense("out", *out, cfg.out_dtype == MLA_F32 ? 4 : 2, rows * 512);
-  if (lse) dense("lse", *lse, 4, rows);
-  if (global) dense("global_seq_lens", *global, 4, B);
-  if (local) dense("local_visible_lens", *local, 4, B * cfg.seq_len_q);
+  dense("page_table", table, at::kInt, B * cfg.page_table_stride);
+  dense("seq_lens", lens, at::kInt, B);
+  if (out) dense("out", *out, os, rows * 512);
+  if (lse) dense("lse", *lse, at::kFloat, rows);
+  if (global) dense("global_seq_lens", *global, at::kInt, B);
+  if (local) dense("local_visible_lens", *local, at::kInt, B * cfg.seq_len_q);
+  // large enough, but laid out in other rows or pages
+  if (qr.dim() == 4 && (qr.size(0) != B || qr.size(1) != cfg.seq_len_q || qr.size(2) != H || qr.size(3) != 64))
+    raise(PyExc_ValueError, "q_rope must be [B, Sq, H, 64] beside q_latent " + shape_of(ql) + ", not " + shape_of(qr));
+  if (pk.dim() == 3 && (pk.size(1) != pc.size(1) || pk.size(2) != 64))
+    raise(PyExc_ValueError, "kpe must be [pages, page_size, 64] beside ckv " + shape_of(pc) + ", not " + shape_of(pk));
+  row_stride("page_table", table, B, cfg.page_table_stride);
+  if (local) row_stride("local_visible_lens", *local, B, cfg.seq_len_q);
   here({&ql, &qr, &pc, &pk, &table, &lens, out, lse, &ws, global, local});
   cfg.global_seq_lens = i32(global);
   cfg.local_visible_lens = i32(local);
   const cudaStream_t stream = a.stream();
   const OnStream on(stream, ql);
   const at::Tensor o = out ? *out
-                           : at::empty({B, cfg.seq_len_q, H, 512},
-                                       ql.options().dtype(cfg.out_dtype == MLA_F32 ? at::kFloat : at::kBFloat16));
+                           : at::empty({B, cfg.seq_len_q, H, 512}, ql.options().dtype(os));
   at::Tensor l;
   if (lse) l = *lse;
   else if (want_lse) l = at::empty({B, cfg.seq_len_q, H}, ql.options().dtype(at::kFloat));

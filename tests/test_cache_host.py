@@ -311,3 +311,55 @@ def test_fork_rejects_tables_whose_entries_pass_32_bits(lib):
     assert status(15, 1 << 27) == n.MLA_ERR_WORKSPACE_TOO_SMALL
     assert status(2049, 1 << 20, page_size=1024) == n.MLA_ERR_UNSUPPORTED
     assert status(1, 1 << 27, B=16384) == n.MLA_ERR_WORKSPACE_TOO_SMALL  # the present rows ask for nothing
+
+
+def test_decode_wrapper_rejects_what_it_would_read_at_the_wrong_place(lib):
+    """Tensors large enough but laid out for another config: each is named, not read at the wrong stride."""
+    from paged_latent_attention_mla_gb300 import PagedMlaDecoder
+
+    def decoder(dtype=BF16, **over):
+        a = dict(H=16, seq_len_q=1, num_pages=6, page_table_stride=3, qkv_dtype=dtype, page_size=16, num_clusters=4, device="cpu")
+        a.update(over)
+        dec = PagedMlaDecoder(**a)
+        dec.plan([20, 40])
+        return dec
+
+    def call(dec, dtype=BF16, B=2, Sq=1, **over):
+        ckv, kpe = pools(dtype=dtype)
+        a = dict(q_latent=torch.zeros((B, Sq, 16, 512), dtype=dtype), q_rope=torch.zeros((B, Sq, 16, 64), dtype=dtype), ckv=ckv,
+                 kpe=kpe, page_table=i32(B, 3), seq_lens=i32(B), scale=1.0)
+        a.update(over)
+        return dec(**a)
+
+    one, two, eight = decoder(), decoder(seq_len_q=2), decoder(F8)
+    for dec, over, error, what in [
+        (one, dict(page_table=i32(2, 4)), ValueError, "page_table"),
+        (one, dict(page_table=torch.zeros((2, 3))), TypeError, "page_table"),
+        (one, dict(seq_lens=torch.zeros(2)), TypeError, "seq_lens"),
+        (one, dict(Sq=2), ValueError, "q_latent"),
+        (two, dict(Sq=2, q_rope=torch.zeros((4, 1, 16, 64), dtype=BF16)), ValueError, "q_rope"),
+        (one, dict(q_rope=torch.zeros((2, 1, 64, 16), dtype=BF16)), ValueError, "q_rope"),
+        (one, dict(kpe=pools(pages=12, P=8)[1]), ValueError, "kpe"),
+        (one, dict(ckv=torch.zeros((6, 16, 1024), dtype=BF16)), ValueError, "ckv"),
+        (one, dict(q_latent=torch.zeros((2, 1, 16, 1024), dtype=BF16)), ValueError, "q_latent"),
+        (one, dict(ckv=torch.zeros((6, 16, 512), dtype=torch.float16)), TypeError, "ckv"),
+        (one, dict(q_latent=torch.zeros((2, 1, 16, 512), dtype=torch.float16)), TypeError, "q_latent"),
+        (one, dict(out=torch.zeros((2, 1, 16, 512), dtype=torch.float16)), TypeError, "out"),
+        (eight, dict(dtype=F8, kpe=torch.zeros((6, 16, 64), dtype=torch.float8_e5m2)), TypeError, "kpe"),
+        (two, dict(Sq=2, local_visible_lens=i32(2, 3)), ValueError, "local_visible_lens"),
+        (one, dict(global_seq_lens=torch.zeros(2)), TypeError, "global_seq_lens"),
+    ]:
+        with pytest.raises(error, match=what):
+            call(dec, **over)
+
+    # what is read where the kernels read it passes these checks and is refused for lying on the CPU
+    for dec, over in [
+        (one, {}), (two, dict(Sq=2, local_visible_lens=i32(2, 2))), (eight, dict(dtype=F8)),
+        (one, dict(page_table=i32(5, 3), seq_lens=i32(5))),  # more rows than the batch
+        (one, dict(page_table=i32(6), q_rope=torch.zeros(2048, dtype=BF16), lse=torch.zeros(32))),  # flat
+        (one, dict(B=1, page_table=i32(1, 9))),  # one row of a wider table
+        (one, dict(ckv=pools(pages=9)[0], kpe=pools(pages=7)[1])),  # pools past num_pages
+        (one, dict(q_latent=torch.zeros((2, 1, 16, 512), dtype=BF16).view(torch.int16))),  # raw bits
+    ]:
+        with pytest.raises(ValueError, match="CUDA tensors"):
+            call(dec, **over)
