@@ -535,8 +535,10 @@ cudaError_t launch_short_variant(const DecodeParams& p, const KvMaps& maps, int 
 template <int RT, bool E4M3>
 int max_clusters(int C) {
   if (cudaFuncSetAttribute(short_decode<RT, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kShortSmem) != cudaSuccess ||
-      cudaFuncSetAttribute(short_decode<RT, E4M3>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+      cudaFuncSetAttribute(short_decode<RT, E4M3>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+    cudaGetLastError();  // the next launch's check is not to find this error
     return 0;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)C, 64);
   cfg.blockDim = dim3(kShortThreads);
@@ -549,7 +551,9 @@ int max_clusters(int C) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   int n = 0;
-  return cudaOccupancyMaxActiveClusters(&n, short_decode<RT, E4M3>, &cfg) == cudaSuccess ? n : 0;
+  if (cudaOccupancyMaxActiveClusters(&n, short_decode<RT, E4M3>, &cfg) == cudaSuccess) return n;
+  cudaGetLastError();
+  return 0;
 }
 
 }  // namespace

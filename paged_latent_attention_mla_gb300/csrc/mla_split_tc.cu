@@ -1302,7 +1302,10 @@ cudaError_t launch_split_kv(const DecodeParams& p, const KvMaps& maps, cudaStrea
 
 int split_kv_max_clusters(int device, bool e4m3) {
   int sms = 0;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
+    cudaGetLastError();  // the next launch's check is not to find this error
+    return 0;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(sms);
   cfg.blockDim = dim3(tc::kThreads);
@@ -1324,8 +1327,9 @@ int split_kv_max_clusters(int device, bool e4m3) {
     cudaFuncSetAttribute(tc::split_kv_tc<false, true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
     e = cudaOccupancyMaxActiveClusters(&n, tc::split_kv_tc<false, true, false>, &cfg);
   }
-  if (e != cudaSuccess || n <= 0) return sms / 2;
-  return n;
+  if (e == cudaSuccess && n > 0) return n;
+  cudaGetLastError();
+  return sms / 2;
 }
 
 }  // namespace mla
