@@ -43,6 +43,18 @@ void check(const char* fn, mla_status_t st) {
   throw Raised{};
 }
 
+// The library's call without the interpreter, as ctypes makes it: a launch waits while the GPU's
+// queue is full.
+struct Released {
+  PyThreadState* held = PyEval_SaveThread();
+  ~Released() { PyEval_RestoreThread(held); }
+};
+template <typename F>
+mla_status_t unlocked(F call) {
+  const Released released;
+  return call();
+}
+
 std::string shape_of(const at::Tensor& t) {
   std::string s = "[";
   for (int64_t d = 0; d < t.dim(); ++d) s += (d ? ", " : "") + std::to_string(t.size(d));
@@ -237,10 +249,12 @@ PyObject* decode(Args a) {
   at::Tensor l;
   if (lse) l = *lse;
   else if (want_lse) l = at::empty({B, cfg.seq_len_q, H}, ql.options().dtype(at::kFloat));
-  check("mla_decode",
-        mla_decode(ql.data_ptr(), qr.data_ptr(), pc.data_ptr(), pk.data_ptr(), i32(table), i32(lens), scale, window,
-                   o.data_ptr(), l.defined() ? static_cast<float*>(l.data_ptr()) : nullptr, ws.data_ptr(),
-                   (size_t)ws.nbytes(), stream, rows_of(ql), (int)H, (int)pc.size(1), &cfg));
+  const int b = rows_of(ql);
+  check("mla_decode", unlocked([&] {
+          return mla_decode(ql.data_ptr(), qr.data_ptr(), pc.data_ptr(), pk.data_ptr(), i32(table), i32(lens), scale, window,
+                            o.data_ptr(), l.defined() ? static_cast<float*>(l.data_ptr()) : nullptr, ws.data_ptr(),
+                            (size_t)ws.nbytes(), stream, b, (int)H, (int)pc.size(1), &cfg);
+        }));
   return tuple_of({o, l});  // an undefined tensor is None
 }
 
@@ -287,8 +301,12 @@ PyObject* append(Args a) {
   o.rope_positions = rope ? (int)rope->size(0) : 0;
   o.global_seq_lens = i32(global);
   const mla_cache_t l = layout(pc, table.size(1), kept);
-  check("mla_cache_append", mla_cache_append(c.data_ptr(), cs, kpe.data_ptr(), ks, i32(start), n, i32(table), i32(lens),
-                                             (int)B, pc.data_ptr(), pk.data_ptr(), &l, &o, status_word(status), a.stream()));
+  uint32_t* word = status_word(status);
+  const cudaStream_t stream = a.stream();
+  check("mla_cache_append", unlocked([&] {
+          return mla_cache_append(c.data_ptr(), cs, kpe.data_ptr(), ks, i32(start), n, i32(table), i32(lens), (int)B,
+                                  pc.data_ptr(), pk.data_ptr(), &l, &o, word, stream);
+        }));
   Py_RETURN_NONE;
 }
 
@@ -320,10 +338,12 @@ PyObject* fork(Args a) {
   const at::Tensor t2 = table_out ? *table_out : fresh(table, {N, W}), l2 = lens_out ? *lens_out : fresh(lens, {N}),
                    r2 = ref_out ? *ref_out : fresh(ref, {pc.size(0)});
   const mla_cache_t l = layout(pc, W, kept);
-  check("mla_cache_fork",
-        mla_cache_fork(i32(table), i32(lens), rows_of(table), i32(parents), i32(add), rows_of(parents), i32(ref),
-                       pc.data_ptr(), pk.data_ptr(), &l, window, sinks, i32(t2), i32(l2), i32(r2), ws.data_ptr(),
-                       (size_t)ws.nbytes(), status_word(status), stream));
+  const int b = rows_of(table), n = rows_of(parents);
+  uint32_t* word = status_word(status);
+  check("mla_cache_fork", unlocked([&] {
+          return mla_cache_fork(i32(table), i32(lens), b, i32(parents), i32(add), n, i32(ref), pc.data_ptr(), pk.data_ptr(), &l,
+                                window, sinks, i32(t2), i32(l2), i32(r2), ws.data_ptr(), (size_t)ws.nbytes(), word, stream);
+        }));
   return tuple_of({t2, l2, r2});
 }
 
@@ -348,9 +368,11 @@ PyObject* compact(Args a) {
   const at::Tensor t2 = table_out ? *table_out : fresh(table, {B, W}), r2 = ref_out ? *ref_out : fresh(ref, {pages}),
                    m2 = map ? *map : fresh(ref, {pages}), u2 = used ? *used : fresh(ref, {1});
   const mla_cache_t l = layout(pc, W);
-  check("mla_cache_compact",
-        mla_cache_compact(i32(table), rows_of(table), i32(ref), pc.data_ptr(), pk.data_ptr(), &l, i32(t2), i32(r2), i32(m2),
-                          i32(u2), ws.data_ptr(), (size_t)ws.nbytes(), stream));
+  const int b = rows_of(table);
+  check("mla_cache_compact", unlocked([&] {
+          return mla_cache_compact(i32(table), b, i32(ref), pc.data_ptr(), pk.data_ptr(), &l, i32(t2), i32(r2), i32(m2), i32(u2),
+                                   ws.data_ptr(), (size_t)ws.nbytes(), stream);
+        }));
   return tuple_of({t2, r2, m2, u2});
 }
 
@@ -373,8 +395,13 @@ PyObject* copy(Args a) {
   ints("dst_pages", dst, {src.size(0)});
   here({&pc, &pk, sc, sk, &src, &dst, status});
   const mla_cache_t l = layout(pc, 1);
-  check("mla_cache_copy", mla_cache_copy(sc->data_ptr(), sk->data_ptr(), rows_of(*sc), pc.data_ptr(), pk.data_ptr(), i32(src),
-                                         i32(dst), rows_of(src), &l, status_word(status), a.stream()));
+  const int pages = rows_of(*sc), n = rows_of(src);
+  uint32_t* word = status_word(status);
+  const cudaStream_t stream = a.stream();
+  check("mla_cache_copy", unlocked([&] {
+          return mla_cache_copy(sc->data_ptr(), sk->data_ptr(), pages, pc.data_ptr(), pk.data_ptr(), i32(src), i32(dst), n, &l,
+                                word, stream);
+        }));
   Py_RETURN_NONE;
 }
 
