@@ -1,4 +1,4 @@
-"""The Python entry points as a program with threads meets them."""
+"""The Python entry points as a program with threads and little memory meets them."""
 
 import sys
 import threading
@@ -6,7 +6,7 @@ import threading
 import pytest
 import torch
 
-from paged_latent_attention_mla_gb300 import cache_copy
+from paged_latent_attention_mla_gb300 import PagedMlaDecoder, cache_copy
 from paged_latent_attention_mla_gb300 import _native as n
 from paged_latent_attention_mla_gb300 import build as nbuild
 
@@ -53,3 +53,25 @@ def test_other_threads_run_while_a_call_is_launched():
     t.join()
     torch.cuda.synchronize()
     assert got == 1
+
+
+def test_outputs_that_do_not_fit_raise_the_out_of_memory_error():
+    """The outputs a call makes are torch's: so is the error when there is no memory for them."""
+    B, H, P = 512, 128, 16
+    ckv, kpe = pools(P=P)
+    table = torch.zeros((B, 1), dtype=torch.int32, device="cuda")
+    lens = torch.ones(B, dtype=torch.int32, device="cuda")
+    ql = torch.zeros((B, 1, H, 512), dtype=torch.bfloat16, device="cuda")
+    qr = torch.zeros((B, 1, H, 64), dtype=torch.bfloat16, device="cuda")
+    dec = PagedMlaDecoder(H=H, seq_len_q=1, num_pages=8, page_table_stride=1, qkv_dtype=torch.bfloat16, page_size=P)
+    dec.plan([1] * B)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction(1e-9)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            dec(ql, qr, ckv, kpe, table, lens, 1.0)
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    out, _ = dec(ql, qr, ckv, kpe, table, lens, 1.0)
+    assert out.shape == (B, 1, H, 512)
