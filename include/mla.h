@@ -205,7 +205,8 @@ MLA_API mla_status_t mla_decode_kernels(int B, int H, int page_size, int window_
  *  workspace  device scratch of at least the planned size, 256-byte aligned.  With
  *             combine_in_kernel, zero it once after allocating it (the rows' arrival
  *             counters must start at zero or hold an earlier call's tag); it needs no
- *             clearing otherwise, nor between calls
+ *             clearing otherwise, nor between calls (only before a captured call is
+ *             replayed after MLA_ERR_TIMEOUT: the replays of a call share its tag)
  *  stream     the CUDA stream all work is enqueued on
  *
  * Cache slots past a request's length and pages no visible key uses may hold

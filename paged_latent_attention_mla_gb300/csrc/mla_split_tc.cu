@@ -315,7 +315,8 @@ __device__ __noinline__ bool tail_group(Misc& M, uint8_t* smem, int own, uint32_
 // In-kernel combine, arrival (the correction warps, 128 threads, once the piece's
 // partial is written): count this CTA's piece of the work row; the last of the row's
 // pieces to arrive combines them.  The counter holds this call's epoch in its high half,
-// so a word left by an earlier call counts as zero.  The last arrival queues the row for
+// so a word left by an earlier call counts as zero; the last arrival leaves zero, so the
+// replays of a captured call, which share its epoch, count anew.  It queues the row for
 // the end of the kernel (every role idle then, so more threads and loads in flight), or
 // asks for the combine now when the queue is full.  The two syncs among the correction
 // warps are mbarriers waited with the bounded waits (phase parity `ph`).  Returns 1 to
@@ -327,14 +328,15 @@ __device__ __noinline__ int arrive_piece(Misc& M, const DecodeParams& p, unsigne
   if ((L & 31) == 0) mbar_arrive(smem_addr(&M.comb_in));
   if (!kwait(M, smem_addr(&M.comb_in), ph)) return -1;
   if (L == 0) {
-    unsigned long long cur = *reinterpret_cast<volatile unsigned long long*>(counter), seen, want;
+    unsigned long long cur = *reinterpret_cast<volatile unsigned long long*>(counter), seen;
+    uint32_t arrived;
     do {
       seen = cur;
-      want = (seen >> 32) == p.epoch ? seen + 1 : ((unsigned long long)p.epoch << 32) | 1ull;
-      cur = atomicCAS(counter, seen, want);
+      arrived = (seen >> 32) == p.epoch ? (uint32_t)seen + 1 : 1u;
+      cur = atomicCAS(counter, seen, arrived == (uint32_t)np ? 0ull : ((unsigned long long)p.epoch << 32) | arrived);
     } while (cur != seen);
     uint32_t now = 0;
-    if ((uint32_t)(want & 0xFFFFFFFFull) == (uint32_t)np) {
+    if (arrived == (uint32_t)np) {
       const uint32_t k = M.ncl++;
       if (k < (uint32_t)kCombList) M.comb_list[k] = make_int4(w, first_slot, np, 0);
       else now = 1;
