@@ -179,11 +179,12 @@ MLA_API mla_status_t mla_plan(const int32_t *seq_lens, int B, int H, int page_si
                       int *split_kv, size_t *workspace_bytes);
 
 /*
- * Kernels one mla_decode of this batch launches.  bf16 calls over few rows and few keys (as
- * the window, or the page table's width, bounds them) run in one kernel, whose clusters join
- * the parts of a row themselves; the others take the split-KV kernel and, unless it combines
- * the pieces itself, the reduction.  num_clusters > 0 and combine_in_kernel always mean the
- * split-KV kernel.
+ * Kernels one mla_decode of this batch launches.  Calls over few rows and few keys (as the
+ * window bounds them, or without one the page table's width, not the lengths) run in one
+ * kernel, whose clusters join the parts of a row themselves; the others take the split-KV
+ * kernel and, unless it combines the pieces itself, the reduction.  How few depends on the
+ * type: e4m3 calls change over earlier.  num_clusters > 0 and combine_in_kernel always mean
+ * the split-KV kernel.
  */
 MLA_API mla_status_t mla_decode_kernels(int B, int H, int page_size, int window_left, const mla_config_t *cfg,
                                         int *kernels);

@@ -131,7 +131,7 @@ int max_groups(int Sq, int page_size, int window_left, const mla_config_t* cfg) 
 //  e4m3: the short-span kernel widens each group (0.7 us), the split-KV kernel reads half the
 //    bytes.  One request of 16 rows over 1024 keys 11.1 us (split-KV 19.6), 32 of 512 13.6 (23.2);
 //    8 of 128 rows over 1024 keys 24.7 (19.5).
-// Over 41 shapes in each type the rule's choice is the fastest or within 9% of it.
+// Over 41 shapes in each type the rule's choice is the fastest or within 6% of it (e4m3: 9%).
 ShortShape short_shape(int B, int H, int page_size, int window_left, const mla_config_t* cfg, int G) {
   ShortShape best{0, 0};
   if (cfg->num_clusters > 0 || cfg->combine_in_kernel) return best;

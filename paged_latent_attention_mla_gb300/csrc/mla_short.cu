@@ -7,7 +7,7 @@
 // no workspace traffic, no second kernel.  A group is loaded once (its latents are K and V both):
 // nine [64 keys x 128 B] blocks by TMA, two groups in flight, read by ldmatrix through the
 // 128-byte swizzle, straight for Q.K^T and transposed for P.V.  The products are warp-level
-// 16-bit MMAs: a group of one row tile has 17 MFLOP at most, and a kernel that small in code
+// 16-bit MMAs: a group of one row tile has 8.9 MFLOP at most, and a kernel that small in code
 // starts in 3 us where the tensor-memory kernel's roles, schedule and teardown take 20.
 //
 // Measured (GB300, back to back): one request of 16 heads over 256, 1024 and 4096 keys 8.9, 9.5
