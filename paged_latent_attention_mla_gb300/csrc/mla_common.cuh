@@ -109,11 +109,13 @@ __host__ __device__ inline void token_range(int K, int Kg, int lvl, bool has_lvl
 struct KeySpan {
   int lo, hi;
 };
-// The union of windows [lo, hi) of a request with K keys.  An empty one begins behind the request's
-// last 64-key group: what lies between the sinks and the window may have been given up, so it must
-// not be looked up for tokens that see sinks only.
-__host__ __device__ __forceinline__ KeySpan key_span(int lo, int hi, int K) {
-  return {lo < hi ? lo : cdiv(K, kKeyGroup) * kKeyGroup, hi};
+// With a window, an empty union (of a request with K keys) begins behind the request's last 64-key
+// group: what lies between the sinks and the window may have been given up, so it must not be
+// looked up for tokens that see sinks only.  (Without one there is nothing to look up; the check
+// alone took 0.9 us on uniform and 1.4 on fp8spec, in every CTA's schedule.)
+template <bool WINDOW>
+__host__ __device__ __forceinline__ KeySpan window_span(KeySpan s, int K) {
+  return {!WINDOW || s.lo < s.hi ? s.lo : cdiv(K, kKeyGroup) * kKeyGroup, s.hi};
 }
 
 // Tiles of a piece of work: tile v holds the 64-key groups 4 v .. 4 v + 3 of its axis.  Without a

@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_decode(const __grid_co
   __syncthreads();
   // this CTA's run of the tile's groups
   const int K = clamp_len(p, b, rank == 0 && tid == 0 ? &M.err : nullptr), Kg = global_len(p, b, K);
-  const KeySpan span = tokens_span(p, b, flat0 / p.H, (min(rows_q, flat0 + kRows) - 1) / p.H, K, Kg);
+  const KeySpan span = window_span<true>(tokens_span(p, b, flat0 / p.H, (min(rows_q, flat0 + kRows) - 1) / p.H, K, Kg), K);
   const Groups g = key_groups(span, p.sinks);
   const int Kv = min(K, span.hi);  // slots and pages from here on no row of the tile sees
   const int per = (g.n + C - 1) / C;

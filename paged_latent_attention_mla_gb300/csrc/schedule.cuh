@@ -44,8 +44,7 @@ __device__ __forceinline__ void token_keys(const DecodeParams& p, int b, int t, 
   token_range(K, Kg, lvl, has_lvl, p.Sq, t, p.causal, p.window_left, p.cp_world, p.cp_rank, p.cp_interleave, lo, hi);
 }
 
-// union of the visible keys of tokens [t0, t1] of request b with local bounds (arbitrary per token);
-// INT_MAX for the lower end where no token has a key in its window
+// union of the visible keys of tokens [t0, t1] of request b with local bounds (arbitrary per token)
 static __device__ __noinline__ int2 tokens_span_lvl(const DecodeParams& p, int b, int t0, int t1, int K, int Kg) {
   int lo_min = INT_MAX, hi_max = 0;
   for (int t = t0; t <= t1; ++t) {
@@ -55,7 +54,7 @@ static __device__ __noinline__ int2 tokens_span_lvl(const DecodeParams& p, int b
     // a token with nothing in its window still sees the sinks below its bound
     if (hi > lo || p.sinks > 0) hi_max = hi > hi_max ? hi : hi_max;
   }
-  return make_int2(lo_min, hi_max);
+  return make_int2(lo_min < hi_max ? lo_min : hi_max, hi_max);
 }
 
 // Union of the visible keys of tokens [t0, t1] of request b.  Without local bounds both ends of
@@ -66,12 +65,12 @@ static __device__ __noinline__ int2 tokens_span_lvl(const DecodeParams& p, int b
 __device__ __forceinline__ KeySpan tokens_span(const DecodeParams& p, int b, int t0, int t1, int K, int Kg) {
   if (p.local_visible_lens) {
     const int2 r = tokens_span_lvl(p, b, t0, t1, K, Kg);
-    return key_span(r.x, r.y, K);
+    return {r.x, r.y};
   }
   int lo0, hi0, lo1, hi1;
   token_range(K, Kg, 0, false, p.Sq, t0, p.causal, p.window_left, p.cp_world, p.cp_rank, p.cp_interleave, lo0, hi0);
   token_range(K, Kg, 0, false, p.Sq, t1, p.causal, p.window_left, p.cp_world, p.cp_rank, p.cp_interleave, lo1, hi1);
-  return key_span(lo0, hi1, K);
+  return {lo0, hi1};
 }
 
 struct Sched {
@@ -81,9 +80,9 @@ struct Sched {
   int Gd;  // groups the tiles are dealt to
 };
 
-// a sub-band's tiles (the union of its work rows), its keys' ends and its axis
+// a sub-band's tiles (the union of its work rows), its first key and its axis
 struct SubSpan {
-  int tile_lo, n, key_lo, key_hi;
+  int tile_lo, n, key_lo;
   TileAxis axis;
 };
 
@@ -93,10 +92,9 @@ __device__ __forceinline__ SubSpan sub_span(const DecodeParams& p, const DealSha
   const int i0 = k * d.wb, i1 = min(d.Qb, i0 + d.wb) - 1;
   int t0, t1;
   work_tokens(i0, i1, p.Sq, p.H, t0, t1);
-  const KeySpan s = tokens_span(p, b, t0, t1, K, Kg);
+  const KeySpan s = window_span<WINDOW>(tokens_span(p, b, t0, t1, K, Kg), K);
   SubSpan u;
   u.key_lo = s.lo;
-  u.key_hi = s.hi;
   u.axis = tile_axis<WINDOW>(s.lo, p.sinks);
   tile_span<WINDOW>(s, u.axis, p.sinks, u.tile_lo, u.n);
   return u;
@@ -108,7 +106,7 @@ __device__ __forceinline__ void work_span(const DecodeParams& p, int b, int i, i
                                           int& n) {
   int t0, t1;
   work_tokens(i, i, p.Sq, p.H, t0, t1);
-  tile_span<WINDOW>(tokens_span(p, b, t0, t1, K, Kg), axis, p.sinks, tlo, n);
+  tile_span<WINDOW>(window_span<WINDOW>(tokens_span(p, b, t0, t1, K, Kg), K), axis, p.sinks, tlo, n);
 }
 
 // Block-wide: fills prefix[0..S] (prefix[S] = T) in shared memory.  scratch needs
@@ -192,6 +190,22 @@ __device__ __forceinline__ int row_parts(const Sched& sc, int pu, int s, int ulo
   return group_of_tile(xl, sc.T, sc.Gd) - g_first + 1;
 }
 
+// With local bounds, pages past every one of a sub-band's are nobody's: its pieces end at the last
+// visible key (without them the request's last token sees its last key).  A pass of its own by the
+// warp that built them: as part of that, it took 1.0 us of fp8spec's kernel, which has no bounds.
+static __device__ __noinline__ void bound_segments(const DecodeParams& p, const DealShape& d, Segment* segs,
+                                                   Segment* overflow, int n) {
+  __syncwarp();
+  for (int i = threadIdx.x & 31; i < n; i += 32) {
+    Segment& sg = i < kSmemSegs ? segs[i] : overflow[i - kSmemSegs];
+    const int b = sg.row() / d.Qb, k = sg.row() % d.Qb / d.wb;
+    int t0, t1;
+    work_tokens(k * d.wb, min(d.Qb, k * d.wb + d.wb) - 1, p.Sq, p.H, t0, t1);
+    sg.K = min(sg.K, tokens_span_lvl(p, b, t0, t1, sg.K, global_len(p, b, sg.K)).y);
+  }
+  __syncwarp();
+}
+
 // Extract the pieces of cluster c, in order: one warp, a lane per super-row of the
 // cluster's share (the spans of a super-row take one read of the request's lengths, and
 // the lanes read theirs together).  The first kSmemSegs go to `segs` in shared memory,
@@ -233,9 +247,7 @@ __device__ __forceinline__ int build_segments(const DecodeParams& p, const Sched
           sg.row_slot = (uint32_t)(b * d.Qb + i) | ((uint32_t)(slot + 1) << 14);
           sg.tile_begin = t_begin;
           sg.tile_end = t_end;
-          // past every local bound the pages are nobody's: the piece ends there (without local
-          // bounds the request's last token sees its last key)
-          sg.K = p.local_visible_lens ? min(K, sub.key_hi) : K;
+          sg.K = K;
           sg.parts = (uint32_t)np | ((uint32_t)(g - g_first) << 16);
           sg.key_lo = sub.key_lo;
           has = true;
@@ -250,6 +262,7 @@ __device__ __forceinline__ int build_segments(const DecodeParams& p, const Sched
     }
     n += __popc(mask);
   }
+  if (p.local_visible_lens) bound_segments(p, d, segs, overflow, n);
   return n;
 }
 

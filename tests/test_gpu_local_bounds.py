@@ -104,3 +104,16 @@ def test_ranks_without_window_keys_read_no_page_given_up(clusters, P):
         lses.append(lse)
     assert given > 0
     check(*merge_ranks(torch.stack(outs), torch.stack(lses)), reference(prob, sinks))
+
+
+@pytest.mark.parametrize("window,sinks", [(-1, 0), (60, 3)])
+def test_segment_lists_past_shared_memory(window, sinks):
+    """600 requests on 2 clusters: more pieces to a cluster than shared memory keeps, each ended by its bound."""
+    lens = [40 + (97 * i) % 260 for i in range(600)]
+    prob = wl.make_problem("uniform", seed=7, H=128, Sq=1, causal=False, window_left=window, page_size=16, seq_lens=lens)
+    lvl = torch.tensor([[1 + (61 * i) % K] for i, K in enumerate(lens)], dtype=torch.int32)
+    d = prob.device_inputs("cuda")
+    table = d["page_table"].tolist()
+    pages = [table[b][j] for b, K in enumerate(lens) for j in range(-(-int(lvl[b, 0]) // 16), -(-K // 16))]
+    nan_page(prob, d, torch.tensor(pages, device="cuda"))
+    check(*run(prob, d, lvl, sinks, 2, num_clusters=2), reference(prob, sinks, lvl))
