@@ -211,7 +211,8 @@ MLA_API mla_status_t mla_decode_kernels(int B, int H, int page_size, int window_
  *  stream     the CUDA stream all work is enqueued on
  *
  * Cache slots past a request's length and pages no visible key uses may hold
- * any bits (NaN included) without affecting the result.
+ * any bits (NaN included) without affecting the result.  (With local_visible_lens,
+ * the keys between the lowest and the highest in its tokens' windows count as used.)
  *
  * Conditions only the device sees (a visible page id outside the pool, a device
  * seq_lens value outside [0, page_table_stride * page_size], a bounded wait that

@@ -105,7 +105,7 @@ __host__ __device__ inline void token_range(int K, int Kg, int lvl, bool has_lvl
 // are below hi.
 
 // Union of tokens' visible ranges: keys [lo, hi) and, with sinks, those below both sinks and hi
-// (hi counts the tokens that see sinks only).
+// (hi counts the sinks of tokens that see sinks only).
 struct KeySpan {
   int lo, hi;
 };

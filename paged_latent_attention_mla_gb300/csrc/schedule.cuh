@@ -51,8 +51,9 @@ static __device__ __noinline__ int2 tokens_span_lvl(const DecodeParams& p, int b
     int lo, hi;
     token_keys(p, b, t, K, Kg, lo, hi);
     if (hi > lo) lo_min = lo < lo_min ? lo : lo_min;
-    // a token with nothing in its window still sees the sinks below its bound
-    if (hi > lo || p.sinks > 0) hi_max = hi > hi_max ? hi : hi_max;
+    // a token with nothing in its window sees the sinks below its bound, and nothing else below it
+    if (hi <= lo) hi = min(hi, p.sinks);
+    hi_max = hi > hi_max ? hi : hi_max;
   }
   return make_int2(lo_min < hi_max ? lo_min : hi_max, hi_max);
 }

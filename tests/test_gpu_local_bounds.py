@@ -117,3 +117,17 @@ def test_segment_lists_past_shared_memory(window, sinks):
     pages = [table[b][j] for b, K in enumerate(lens) for j in range(-(-int(lvl[b, 0]) // 16), -(-K // 16))]
     nan_page(prob, d, torch.tensor(pages, device="cuda"))
     check(*run(prob, d, lvl, sinks, 2, num_clusters=2), reference(prob, sinks, lvl))
+
+
+@pytest.mark.parametrize("H,clusters,kernels", [(8, 0, 1), (8, 76, 2), (128, 3, 2)])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_bounds_of_tokens_that_see_sinks_only_load_nothing(H, clusters, kernels, dtype):
+    """A bound past the last key that the other tokens' windows hold, and below its own token's floor."""
+    lvl = torch.tensor([[703] + [1] * 14 + [714], [0] * 15 + [715], [707] + [90] * 15], dtype=torch.int32)
+    prob = wl.make_problem("uniform", seed=8, H=H, Sq=16, causal=False, window_left=5, dtype=dtype, page_size=8,
+                           seq_lens=[721] * 3)  # the floor of token t is 700 + t
+    d = prob.device_inputs("cuda")
+    for b, first in ((0, 704), (1, 64), (2, 712)):  # request 1 sees its 63 sinks only
+        for j in range(first // 8, 91):
+            nan_page(prob, d, int(d["page_table"][b, j]))
+    check(*run(prob, d, lvl, 63, kernels, num_clusters=clusters), reference(prob, 63, lvl))
