@@ -189,7 +189,7 @@ int plan_max_parts(const int32_t* seq_lens, int B, int H, int page_size, int win
       if (hi > lo) lo_min = std::min(lo_min, lo);
       if (hi > lo || sinks > 0) hi_max = std::max(hi_max, hi);
     }
-    return window_span<WINDOW>({std::min(lo_min, hi_max), hi_max}, K);
+    return window_span<WINDOW>({std::min(lo_min, hi_max), hi_max, K}, K);
   };
   if (sh.ctas > 0) {
     const int rows_q = Sq * H, R = sh.rows;

@@ -105,9 +105,10 @@ __host__ __device__ inline void token_range(int K, int Kg, int lvl, bool has_lvl
 // are below hi.
 
 // Union of tokens' visible ranges: keys [lo, hi) and, with sinks, those below both sinks and hi
-// (hi counts the sinks of tokens that see sinks only).
+// (hi counts the sinks of tokens that see sinks only).  Slots from `end` on (the length, or with
+// local bounds where the pages of visible keys end) are not read.
 struct KeySpan {
-  int lo, hi;
+  int lo, hi, end;
 };
 // With a window, an empty union (of a request with K keys) begins behind the request's last 64-key
 // group: what lies between the sinks and the window may have been given up, so it must not be
@@ -115,7 +116,7 @@ struct KeySpan {
 // alone took 0.9 us on uniform and 1.4 on fp8spec, in every CTA's schedule.)
 template <bool WINDOW>
 __host__ __device__ __forceinline__ KeySpan window_span(KeySpan s, int K) {
-  return {!WINDOW || s.lo < s.hi ? s.lo : cdiv(K, kKeyGroup) * kKeyGroup, s.hi};
+  return {!WINDOW || s.lo < s.hi ? s.lo : cdiv(K, kKeyGroup) * kKeyGroup, s.hi, s.end};
 }
 
 // Tiles of a piece of work: tile v holds the 64-key groups 4 v .. 4 v + 3 of its axis.  Without a
@@ -282,7 +283,7 @@ struct RowInfo {
 
 // One piece of work of a cluster.  The work row (< 2^14) and the partial slot + 1 (0: the
 // row's only piece, written to the output) share one word; K is the request's local key
-// count, or the sub-band's last visible key + 1 with local bounds, so the roles start a piece
+// count, or where its read pages end with local bounds (KeySpan), so the roles start a piece
 // without reading seq_lens.
 struct Segment {
   uint32_t row_slot;   // row | (slot + 1) << 14

@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_decode(const __grid_co
   const int K = clamp_len(p, b, rank == 0 && tid == 0 ? &M.err : nullptr), Kg = global_len(p, b, K);
   const KeySpan span = window_span<true>(tokens_span(p, b, flat0 / p.H, (min(rows_q, flat0 + kRows) - 1) / p.H, K, Kg), K);
   const Groups g = key_groups(span, p.sinks);
-  const int Kv = min(K, span.hi);  // slots and pages from here on no row of the tile sees
+  const int Kv = span.end;
   const int per = (g.n + C - 1) / C;
   const int v0 = min(g.n, rank * per), v1 = min(g.n, v0 + per), n = v1 - v0;
   const int parts = per > 0 ? (g.n + per - 1) / per : 0;  // CTAs of the cluster with groups
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_decode(const __grid_co
     if (i == 0) mbar_try_wait(smem_addr(&M.q_full), 0);
     mbar_try_wait(bar, (i >> 1) & 1);
     const int key0 = g.at(v0 + i) * kKeyGroup;
-    // slots past the last visible key: any bits there must not reach P.c
+    // slots past the keys that are read: any bits there must not reach P.c
     if constexpr (E4M3) {
       if (i == 0) {
         widen<1>(smem + kOffK, smem, 64, tid);

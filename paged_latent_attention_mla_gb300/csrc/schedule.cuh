@@ -66,12 +66,14 @@ static __device__ __noinline__ int2 tokens_span_lvl(const DecodeParams& p, int b
 __device__ __forceinline__ KeySpan tokens_span(const DecodeParams& p, int b, int t0, int t1, int K, int Kg) {
   if (p.local_visible_lens) {
     const int2 r = tokens_span_lvl(p, b, t0, t1, K, Kg);
-    return {r.x, r.y};
+    // pages past every bound are nobody's, so the reads end at the last visible key; where its page
+    // is the request's last there are none, and they end at the length as without bounds
+    return {r.x, r.y, (r.y - 1) >> p.page_shift < (K - 1) >> p.page_shift ? r.y : K};
   }
   int lo0, hi0, lo1, hi1;
   token_range(K, Kg, 0, false, p.Sq, t0, p.causal, p.window_left, p.cp_world, p.cp_rank, p.cp_interleave, lo0, hi0);
   token_range(K, Kg, 0, false, p.Sq, t1, p.causal, p.window_left, p.cp_world, p.cp_rank, p.cp_interleave, lo1, hi1);
-  return {lo0, hi1};
+  return {lo0, hi1, K};
 }
 
 struct Sched {
@@ -81,9 +83,9 @@ struct Sched {
   int Gd;  // groups the tiles are dealt to
 };
 
-// a sub-band's tiles (the union of its work rows), its first key and its axis
+// a sub-band's tiles (the union of its work rows), its first key, where its keys end and its axis
 struct SubSpan {
-  int tile_lo, n, key_lo;
+  int tile_lo, n, key_lo, end;
   TileAxis axis;
 };
 
@@ -96,6 +98,7 @@ __device__ __forceinline__ SubSpan sub_span(const DecodeParams& p, const DealSha
   const KeySpan s = window_span<WINDOW>(tokens_span(p, b, t0, t1, K, Kg), K);
   SubSpan u;
   u.key_lo = s.lo;
+  u.end = s.end;
   u.axis = tile_axis<WINDOW>(s.lo, p.sinks);
   tile_span<WINDOW>(s, u.axis, p.sinks, u.tile_lo, u.n);
   return u;
@@ -191,22 +194,6 @@ __device__ __forceinline__ int row_parts(const Sched& sc, int pu, int s, int ulo
   return group_of_tile(xl, sc.T, sc.Gd) - g_first + 1;
 }
 
-// With local bounds, pages past every one of a sub-band's are nobody's: its pieces end at the last
-// visible key (without them the request's last token sees its last key).  A pass of its own by the
-// warp that built them: as part of that, it took 1.0 us of fp8spec's kernel, which has no bounds.
-static __device__ __noinline__ void bound_segments(const DecodeParams& p, const DealShape& d, Segment* segs,
-                                                   Segment* overflow, int n) {
-  __syncwarp();
-  for (int i = threadIdx.x & 31; i < n; i += 32) {
-    Segment& sg = i < kSmemSegs ? segs[i] : overflow[i - kSmemSegs];
-    const int b = sg.row() / d.Qb, k = sg.row() % d.Qb / d.wb;
-    int t0, t1;
-    work_tokens(k * d.wb, min(d.Qb, k * d.wb + d.wb) - 1, p.Sq, p.H, t0, t1);
-    sg.K = min(sg.K, tokens_span_lvl(p, b, t0, t1, sg.K, global_len(p, b, sg.K)).y);
-  }
-  __syncwarp();
-}
-
 // Extract the pieces of cluster c, in order: one warp, a lane per super-row of the
 // cluster's share (the spans of a super-row take one read of the request's lengths, and
 // the lanes read theirs together).  The first kSmemSegs go to `segs` in shared memory,
@@ -248,7 +235,7 @@ __device__ __forceinline__ int build_segments(const DecodeParams& p, const Sched
           sg.row_slot = (uint32_t)(b * d.Qb + i) | ((uint32_t)(slot + 1) << 14);
           sg.tile_begin = t_begin;
           sg.tile_end = t_end;
-          sg.K = K;
+          sg.K = sub.end;
           sg.parts = (uint32_t)np | ((uint32_t)(g - g_first) << 16);
           sg.key_lo = sub.key_lo;
           has = true;
@@ -263,7 +250,6 @@ __device__ __forceinline__ int build_segments(const DecodeParams& p, const Sched
     }
     n += __popc(mask);
   }
-  if (p.local_visible_lens) bound_segments(p, d, segs, overflow, n);
   return n;
 }
 
