@@ -49,10 +49,10 @@ ALL = ["uniform", "varlen", "fp8spec", "window"]
 # the kernel sources it was taken on: reported when their hash still matches, else null.
 KERNEL_SOURCES = ("mla_split_tc.cu", "mla_common.cuh", "schedule.cuh", "tma_pages.cuh", "ptx.cuh")
 NCU_TRAFFIC = {
-    "uniform": {"sources_sha256": "f0538ce68233b3dbbd3d0440f7d09dd205e000f0e3f9f2a3aa69bdc2ccb621cf", "bytes": 322659328 + 8032768},
-    "varlen": {"sources_sha256": "f0538ce68233b3dbbd3d0440f7d09dd205e000f0e3f9f2a3aa69bdc2ccb621cf", "bytes": 558262784 + 15718144},
-    "fp8spec": {"sources_sha256": "f0538ce68233b3dbbd3d0440f7d09dd205e000f0e3f9f2a3aa69bdc2ccb621cf", "bytes": 310197504 + 8612864},
-    "window": {"sources_sha256": "f0538ce68233b3dbbd3d0440f7d09dd205e000f0e3f9f2a3aa69bdc2ccb621cf", "bytes": 43287552 + 636928},
+    "uniform": {"sources_sha256": "ef9310493dc0d3536f2f08ff5270e1de64699ab9b8c7488f93f813e68fe41665", "bytes": 322583296 + 7560704},
+    "varlen": {"sources_sha256": "ef9310493dc0d3536f2f08ff5270e1de64699ab9b8c7488f93f813e68fe41665", "bytes": 558726656 + 15559424},
+    "fp8spec": {"sources_sha256": "ef9310493dc0d3536f2f08ff5270e1de64699ab9b8c7488f93f813e68fe41665", "bytes": 310206976 + 8817152},
+    "window": {"sources_sha256": "ef9310493dc0d3536f2f08ff5270e1de64699ab9b8c7488f93f813e68fe41665", "bytes": 43287552 + 655104},
 }
 
 
