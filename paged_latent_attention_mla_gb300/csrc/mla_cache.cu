@@ -130,10 +130,11 @@ __device__ __forceinline__ int row_of_token(const int32_t* start, int B, int i, 
 // lane k runs the chain of token k of up to 32 at once, while the first latents are on their way
 // into the warp's ring in shared memory; then token by token, kAhead rows ahead of the one at
 // hand, each lane reading back what it copied itself.
-// Measured: 65.5k prompt tokens, bf16 into e4m3 pages with norm and rotation, 25.9 us (130 MB,
-// 5.0 TB/s; a warp to a token 31.8, four tokens held in a warp's registers 28 to 36 over the
+// Measured: 65.5k prompt tokens, bf16 into e4m3 pages with norm and rotation, 27.1 us (130 MB,
+// 4.8 TB/s; a warp to a token 31.8, four tokens held in a warp's registers 28 to 36 over the
 // occupancies).  What is left over the 19.2 us of its bytes is the start of the one wave (3 us of
-// lookups) and the scattered stores.  64 tokens of a decode step: 3.1 us, the chain.
+// lookups) and its instructions (52% of the issue slots, beside 45% of HBM).  64 tokens of a
+// decode step: 3.2 us, the chain.
 constexpr int kAppendThreads = 256, kAppendWarps = kAppendThreads / 32, kAppendWave = 4;
 
 template <typename In, bool E4M3>
@@ -523,9 +524,9 @@ __device__ __forceinline__ bool is_claim(int count) { return count < INT_MIN + k
 //   3  the fresh pages each row needs, free pages counted
 //   4  each row's place in the free list, and the list (free pages in ascending order)
 // All sums are integer sums and minima: the result does not depend on their order.
-// Measured, with the kernel after it: 128 rows over 16384 pages, most going on, 8.8 us, of which
+// Measured, with the kernel after it: 128 rows over 16384 pages, most going on, 8.9 us, of which
 // the phases' round trips to L2 (0.5 us each) and three barriers (0.6 to 0.9 us with the writes
-// they wait for) are 7; 256 beams over 65536 pages 12.5 us (on 8 CTAs 14.7 and more: the
+// they wait for) are 7; 256 beams over 65536 pages 12.8 us (on 8 CTAs 14.7 and more: the
 // scattered count updates and the scan of the counts go by the SM).
 __global__ void __launch_bounds__(kPlanThreads, 1) fork_plan_kernel(const __grid_constant__ ForkParams p) {
   __shared__ Kids s_kids[kPlanThreads];
@@ -772,8 +773,8 @@ __global__ void __launch_bounds__(256) fork_rows_kernel(const __grid_constant__ 
 // ------------------------------------------------------------------ compact
 // One cluster: the pages in use (n of them) are counted; the m-th of those at n or above goes
 // to the m-th free page below n.  Phases as in the fork, a cluster barrier between them.
-// Measured with the moves: 500 pages 6.9 us, a pool of 16384 64-key bf16 pages half in use
-// (4096 of them moved, 605 MB) 96.8 us (6.2 TB/s).
+// Measured with the moves: 500 pages 7.2 us, a pool of 16384 64-key bf16 pages half in use
+// (4096 of them moved, 605 MB) 97.0 us (6.2 TB/s).
 __global__ void __launch_bounds__(kPlanThreads, 1) compact_plan_kernel(const __grid_constant__ CompactParams p) {
   __shared__ int part[32], s_below;
   __shared__ int2 s_sums[kPlanCtas];
