@@ -171,7 +171,7 @@ ShortShape short_shape(int B, int H, int page_size, int window_left, const mla_c
 // local bounds (whose device values the host does not have) every local key is taken
 // as visible, which makes the count an estimate.
 // sh.ctas > 0: the parts of the short-span kernel's clusters instead.
-template <bool WINDOW>
+template <int SPAN>
 int plan_max_parts(const int32_t* seq_lens, int B, int H, int page_size, int window_left, const mla_config_t* cfg,
                    int G, ShortShape sh) {
   const int Sq = cfg->seq_len_q;
@@ -189,7 +189,7 @@ int plan_max_parts(const int32_t* seq_lens, int B, int H, int page_size, int win
       if (hi > lo) lo_min = std::min(lo_min, lo);
       if (hi > lo || sinks > 0) hi_max = std::max(hi_max, hi);
     }
-    return window_span<WINDOW>({std::min(lo_min, hi_max), hi_max, K}, K);
+    return window_span<SPAN>({std::min(lo_min, hi_max), hi_max, K}, K);
   };
   if (sh.ctas > 0) {
     const int rows_q = Sq * H, R = sh.rows;
@@ -209,8 +209,8 @@ int plan_max_parts(const int32_t* seq_lens, int B, int H, int page_size, int win
     int t0, t1;
     work_tokens(k * d.wb, std::min(d.Qb, k * d.wb + d.wb) - 1, Sq, H, t0, t1);
     const KeySpan u = keys(b, t0, t1);
-    axis[s] = tile_axis<WINDOW>(u.lo, sinks);
-    tile_span<WINDOW>(u, axis[s], sinks, ulo[s], U[s]);
+    axis[s] = tile_axis<SPAN>(u.lo, sinks);
+    tile_span<SPAN>(u, axis[s], sinks, ulo[s], U[s]);
     prefix[s + 1] = prefix[s] + (U[s] > 0 ? pu + kUnitsPerTile * U[s] : 0);
   }
   const long long T = prefix[d.S];
@@ -220,7 +220,7 @@ int plan_max_parts(const int32_t* seq_lens, int B, int H, int page_size, int win
     const int b = w / d.Qb, i = w % d.Qb, s = b * d.nsub + i / d.wb;
     int t0, t1, tlo, n;
     work_tokens(i, i, Sq, H, t0, t1);
-    tile_span<WINDOW>(keys(b, t0, t1), axis[s], sinks, tlo, n);
+    tile_span<SPAN>(keys(b, t0, t1), axis[s], sinks, tlo, n);
     if (n <= 0) continue;
     const long long xf = tile_unit(prefix[s], pu, tlo - ulo[s]), xl = tile_unit(prefix[s], pu, tlo - ulo[s] + n - 1);
     most = std::max(most, group_of_tile(xl, T, Gd) - group_of_tile(xf, T, Gd) + 1);
@@ -360,8 +360,9 @@ mla_status_t mla_plan(const int32_t* seq_lens, int B, int H, int page_size, int 
   int G;
   if (resolve_clusters(cfg, cfg->qkv_dtype == MLA_E4M3, &G) != 0) return MLA_ERR_CUDA;
   const ShortShape sh = short_shape(B, H, page_size, window_left, cfg, G);
-  *split_kv = window_left >= 0 ? plan_max_parts<true>(seq_lens, B, H, page_size, window_left, cfg, G, sh)
-                               : plan_max_parts<false>(seq_lens, B, H, page_size, window_left, cfg, G, sh);
+  // a window without sinks deals the same tiles as the whole sequence
+  *split_kv = sinks_of(cfg, window_left) > 0 ? plan_max_parts<kSinks>(seq_lens, B, H, page_size, window_left, cfg, G, sh)
+                                             : plan_max_parts<kWhole>(seq_lens, B, H, page_size, window_left, cfg, G, sh);
   *workspace_bytes = ws_layout(B, cfg->seq_len_q, H, G, cfg->partial_fp16 ? 1 : 0).total;
   return MLA_OK;
 }

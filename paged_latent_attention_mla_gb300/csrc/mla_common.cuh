@@ -110,30 +110,35 @@ __host__ __device__ inline void token_range(int K, int Kg, int lvl, bool has_lvl
 struct KeySpan {
   int lo, hi, end;
 };
-// With a window, an empty union (of a request with K keys) begins behind the request's last 64-key
+
+// What a decode's tokens see, a variant of the split-KV kernel each: every key (below their bounds),
+// a window, or a window and sinks.  What a variant does not need costs it: with one variant for
+// both kinds of windows, those without sinks took 58.7 us for 56.2 on the benchmark's batch.
+constexpr int kWhole = 0, kWindow = 1, kSinks = 2;
+
+// With sinks, an empty union (of a request with K keys) begins behind the request's last 64-key
 // group: what lies between the sinks and the window may have been given up, so it must not be
-// looked up for tokens that see sinks only.  (Without one there is nothing to look up; the check
+// looked up for tokens that see sinks only.  (Otherwise there is nothing to look up; the check
 // alone took 0.9 us on uniform and 1.4 on fp8spec, in every CTA's schedule.)
-template <bool WINDOW>
+template <int SPAN>
 __host__ __device__ __forceinline__ KeySpan window_span(KeySpan s, int K) {
-  return {!WINDOW || s.lo < s.hi ? s.lo : cdiv(K, kKeyGroup) * kKeyGroup, s.hi, s.end};
+  return {SPAN != kSinks || s.lo < s.hi ? s.lo : cdiv(K, kKeyGroup) * kKeyGroup, s.hi, s.end};
 }
 
-// Tiles of a piece of work: tile v holds the 64-key groups 4 v .. 4 v + 3 of its axis.  Without a
-// window the axis is the sequence.  With one, the groups between the last that holds a sink
+// Tiles of a piece of work: tile v holds the 64-key groups 4 v .. 4 v + 3 of its axis.  Without
+// sinks the axis is the sequence.  With them, the groups between the last that holds a sink
 // and the window's first are left out: group i is the sequence's from number ns on the
-// (i + jump)th, so the sinks share the window's first tile.  (Without sinks the window begins
-// on a tile of the sequence.)  The numbering is the sub-band's (its work rows walk the same
+// (i + jump)th, so the sinks share the window's first tile.  The numbering is the sub-band's (its work rows walk the same
 // tiles together).
 constexpr int kTileGroups = kTileN / kKeyGroup;
 struct TileAxis {
   int ns, jump;
 };
-template <bool WINDOW>
+template <int SPAN>
 __host__ __device__ __forceinline__ TileAxis tile_axis(int sub_lo, int sinks) {
   TileAxis a{0, 0};
-  if (WINDOW) {
-    const int first = sinks > 0 ? sub_lo / kKeyGroup : sub_lo / kTileN * kTileGroups;
+  if (SPAN == kSinks) {
+    const int first = sub_lo / kKeyGroup;
     const int st = (sinks + kKeyGroup - 1) / kKeyGroup;
     a.ns = st < first ? st : first;
     a.jump = first - a.ns;
@@ -141,22 +146,22 @@ __host__ __device__ __forceinline__ TileAxis tile_axis(int sub_lo, int sinks) {
   return a;
 }
 // the sequence's number of group i of the axis
-template <bool WINDOW>
+template <int SPAN>
 __host__ __device__ __forceinline__ int seq_group(TileAxis a, int i) {
-  return WINDOW && i >= a.ns ? i + a.jump : i;
+  return SPAN == kSinks && i >= a.ns ? i + a.jump : i;
 }
 
 // tiles [tile_lo, tile_lo + n) of the axis hold the keys of s
-template <bool WINDOW>
+template <int SPAN>
 __host__ __device__ __forceinline__ void tile_span(KeySpan s, TileAxis a, int sinks, int& tile_lo, int& n_tiles) {
   tile_lo = n_tiles = 0;
-  if (WINDOW && sinks > 0) {
+  if (SPAN == kSinks) {
     if (s.hi <= 0) return;
     const int end = (s.hi + kKeyGroup - 1) / kKeyGroup;
     n_tiles = cdiv(end > a.ns + a.jump ? end - a.jump : (end < a.ns ? end : a.ns), kTileGroups);
   } else if (s.hi > s.lo) {
-    tile_lo = s.lo / kTileN - a.jump / kTileGroups;
-    n_tiles = (s.hi + kTileN - 1) / kTileN - a.jump / kTileGroups - tile_lo;
+    tile_lo = s.lo / kTileN;
+    n_tiles = (s.hi + kTileN - 1) / kTileN - tile_lo;
   }
 }
 

@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(256) debug_gather_kernel(const __grid_constant
       int pg, rw, shift = 0;
       bool bad;
       while ((1 << shift) < page_size) ++shift;
-      box_page<false>(page_table, pt_stride, num_pages, shift, b, key0 + i * br, br, 0, 0, K, pg, rw, bad);
+      box_page<kWhole>(page_table, pt_stride, num_pages, shift, b, key0 + i * br, br, 0, 0, K, pg, rw, bad);
       if (bad && err) atomicOr(err, kErrBadPage);
       for (int kb = 0; kb < nlat; ++kb)
         tma_load_3d(smem_addr(smem + kb * kBlockBytes + i * br * 128), &maps.ckv, kb * blk_elems<E4M3>(), rw, pg,

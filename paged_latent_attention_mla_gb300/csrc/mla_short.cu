@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_decode(const __grid_co
   __syncthreads();
   // this CTA's run of the tile's groups
   const int K = clamp_len(p, b, rank == 0 && tid == 0 ? &M.err : nullptr), Kg = global_len(p, b, K);
-  const KeySpan span = window_span<true>(tokens_span(p, b, flat0 / p.H, (min(rows_q, flat0 + kRows) - 1) / p.H, K, Kg), K);
+  const KeySpan span = window_span<kSinks>(tokens_span(p, b, flat0 / p.H, (min(rows_q, flat0 + kRows) - 1) / p.H, K, Kg), K);
   const Groups g = key_groups(span, p.sinks);
   const int Kv = span.end;
   const int per = (g.n + C - 1) / C;
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kShortThreads, 1) short_decode(const __grid_co
   auto look_up = [&](int i) {
     if (i >= n || lane >= nb) return;
     bool miss;
-    box_page<true>(p.page_table, p.pt_stride, p.num_pages, p.page_shift, b, g.at(v0 + i) * kKeyGroup + lane * br, br,
+    box_page<kSinks>(p.page_table, p.pt_stride, p.num_pages, p.page_shift, b, g.at(v0 + i) * kKeyGroup + lane * br, br,
                    span.lo, p.sinks, Kv, pg, rw, miss);
     bad |= miss;
   };

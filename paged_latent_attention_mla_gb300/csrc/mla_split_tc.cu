@@ -437,14 +437,14 @@ __device__ __noinline__ void combine_row(const DecodeParams& p, const uint8_t* p
 // Fused combine: the work rows with no visible key in any of their M rows have no piece;
 // this CTA's share of them (every gridDim.x-th) gets O = 0 and LSE = -inf (the correction
 // warps, 128 threads, one M row each).  Out of line: once per kernel.
-template <bool WINDOW>
+template <int SPAN>
 __device__ __noinline__ void write_empty_rows(const DecodeParams& p, const DealShape& DS, int L) {
   const int rows_q = p.Sq * p.H;
   for (int w = blockIdx.x; w < DS.Rw; w += gridDim.x) {
     const int b = w / DS.Qb, i = w % DS.Qb;
     const int K = clamp_len(p, b, nullptr);
     int tlo, n;
-    work_span<WINDOW>(p, b, i, K, global_len(p, b, K), TileAxis{0, 0}, tlo, n);  // empty on any axis alike
+    work_span<SPAN>(p, b, i, K, global_len(p, b, K), TileAxis{0, 0}, tlo, n);  // empty on any axis alike
     if (n > 0) continue;
     const int flat = kTileM * i + L;
     if (flat >= rows_q) continue;
@@ -541,9 +541,9 @@ __device__ __noinline__ void piece_epilogue(const DecodeParams& p, uint8_t* slot
 }
 
 // E4M3: e4m3 inputs (else bf16).  ONE_BOX: page_size >= 64, one page box per 64-key group
-// (else 64 / page_size boxes, looked up through the loader's shared table).  WINDOW: a sliding window,
-// with or without sinks; its tiles are numbered without what lies before it (the sinks' aside).
-template <bool E4M3, bool ONE_BOX, bool WINDOW>
+// (else 64 / page_size boxes, looked up through the loader's shared table).  SPAN: kWhole, kWindow
+// or kSinks.
+template <bool E4M3, bool ONE_BOX, int SPAN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     split_kv_tc(const __grid_constant__ DecodeParams p, const __grid_constant__ KvMaps maps) {
   using C = Cfg<E4M3>;
@@ -607,14 +607,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   {
     // the batch schedule, in the ring memory before any tile lands there
     int32_t* scratch = reinterpret_cast<int32_t*>(smem + C::kOffRing);
-    Sched sc = build_schedule<WINDOW>(p, scratch, &M.err);
+    Sched sc = build_schedule<SPAN>(p, scratch, &M.err);
     // this CTA's pieces first (every role waits for them), then the row table's share
     // (measured: the other order held the segments back by 1.6 us)
     if (warp == 0) {
-      const int nseg = build_segments<WINDOW>(p, sc, cl, segs, overflow);
+      const int nseg = build_segments<SPAN>(p, sc, cl, segs, overflow);
       if (lane == 0) M.nseg = nseg;
     }
-    if (blockIdx.x * blockDim.x < DS.Rw) write_row_table<WINDOW>(p, sc);  // the CTAs that own rows of the table
+    if (blockIdx.x * blockDim.x < DS.Rw) write_row_table<SPAN>(p, sc);  // the CTAs that own rows of the table
   }
   __syncthreads();
   tc_fence_before();
@@ -624,7 +624,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = M.tmem_base;
   const int nseg = M.nseg;
   auto lead = [&](uint64_t& bar) { return map_to_rank(smem_addr(&bar), 0); };
-  auto axis_of = [&](const Segment& sg) { return tile_axis<WINDOW>(sg.key_lo, p.sinks); };
+  auto axis_of = [&](const Segment& sg) { return tile_axis<SPAN>(sg.key_lo, p.sinks); };
   auto seg_at = [&](int s) -> Segment { return s < kSmemSegs ? segs[s] : overflow[s - kSmemSegs]; };
 
   if (warp < 4) {
@@ -642,7 +642,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int key_lo = 0, key_hi = 0;
       if (flat < rows_q) {
         // the window's floor is taken on the whole length, which sg.K is not with local bounds
-        const int Kw = WINDOW && p.local_visible_lens ? clamp_len(p, b, nullptr) : sg.K;
+        const int Kw = SPAN != kWhole && p.local_visible_lens ? clamp_len(p, b, nullptr) : sg.K;
         token_keys(p, b, flat / p.H, sg.K, global_len(p, b, Kw), key_lo, key_hi);
       }
       const int n = sg.tile_end - sg.tile_begin;
@@ -654,20 +654,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_after();
         // this thread's 128 keys: two groups, consecutive but where the axis jumps
         const int grp = (sg.tile_begin + i) * kTileGroups + 2 * half;
-        const int key0 = seq_group<WINDOW>(ax, grp) * kKeyGroup, key1 = seq_group<WINDOW>(ax, grp + 1) * kKeyGroup;
+        const int key0 = seq_group<SPAN>(ax, grp) * kKeyGroup, key1 = seq_group<SPAN>(ax, grp + 1) * kKeyGroup;
         const bool full = key0 >= key_lo && key1 + kKeyGroup <= key_hi;
         const uint32_t sbase_t = tmem + lanebase + st * 128;
         // visible keys of this thread's 128 (all of them on most tiles): [vlo, vhi) relative to
-        // key0, with a window the sinks too.  On a masked tile they are a word of bits per chunk, one test a key; without a window e4m3 keeps one unsigned compare a key, so the
-        // loops stay branch-free (measured, bits against compare: uniform 98.9 and 99.6 us,
-        // varlen 151.5 and 152.1, but fp8spec 171.0 and 165.0)
+        // key0, beside the sinks.  On a masked tile they are a word of bits per chunk, one test a
+        // key; without sinks e4m3 keeps one unsigned compare a key, so the loops stay branch-free
+        // (measured, bits against compare: uniform 98.9 and 99.6 us, varlen 151.5 and 152.1, but
+        // fp8spec 171.0 and 165.0)
         const int vlo = full ? 0 : min(max(key_lo - key0, 0), 128);
         const int vhi = full ? 128 : min(max(key_hi - key0, 0), 128);
         const uint32_t vspan = static_cast<uint32_t>(max(vhi - vlo, 0));
-        constexpr bool kBits = WINDOW || !E4M3;
+        constexpr bool kBits = SPAN == kSinks || !E4M3;
         auto chunk_bits = [&](int ch) -> uint32_t {
           if constexpr (!kBits) return 0u;
-          if constexpr (!WINDOW) return bits_below(vhi - 32 * ch) & ~bits_below(vlo - 32 * ch);
+          if constexpr (SPAN != kSinks) return bits_below(vhi - 32 * ch) & ~bits_below(vlo - 32 * ch);
           const int c0 = (ch < 2 ? key0 : key1) + 32 * (ch & 1);  // the chunk's first key
           return bits_below(key_hi - c0) & (~bits_below(key_lo - c0) | bits_below(p.sinks - c0));
         };
@@ -908,7 +909,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
     }
-    if (ok && p.fused_combine) write_empty_rows<WINDOW>(p, DS, L);
+    if (ok && p.fused_combine) write_empty_rows<SPAN>(p, DS, L);
   } else if (warp == 8) {
     // ------------------------------------------------------------ MMA issue (leader CTA)
     if (rank == 0 && lane == 0) {
@@ -971,7 +972,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int it = 0; it < C::kVItems; ++it)
             if (!take(va[it], slot[it])) return false;
-          if (seq_group<WINDOW>(ax, kTileGroups * tile + vp) == ngroups - 1 && tail_rows != 0) {
+          if (seq_group<SPAN>(ax, kTileGroups * tile + vp) == ngroups - 1 && tail_rows != 0) {
             // the request's last key group: the peer zeroed its slots' tail too
             if (!kwait(M, smem_addr(&M.tail_ready[tcount & 1]), (tcount >> 1) & 1)) return false;
             ++tcount;
@@ -1084,14 +1085,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if constexpr (one_box) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          box_page<WINDOW>(p.page_table, p.pt_stride, p.num_pages, p.page_shift, b,
-                   seq_group<WINDOW>(ax, tile * kTileGroups + q) * kKeyGroup, kKeyGroup, key_lo, p.sinks, K, tb.pg[q],
+          box_page<SPAN>(p.page_table, p.pt_stride, p.num_pages, p.page_shift, b,
+                   seq_group<SPAN>(ax, tile * kTileGroups + q) * kKeyGroup, kKeyGroup, key_lo, p.sinks, K, tb.pg[q],
                    tb.rw[q], bad);
           bad_page |= bad;
         }
       } else if (lane < 4 * nb) {
-        box_page<WINDOW>(p.page_table, p.pt_stride, p.num_pages, p.page_shift, b,
-                 seq_group<WINDOW>(ax, tile * kTileGroups + lane / nb) * kKeyGroup + lane % nb * br, br, key_lo, p.sinks, K,
+        box_page<SPAN>(p.page_table, p.pt_stride, p.num_pages, p.page_shift, b,
+                 seq_group<SPAN>(ax, tile * kTileGroups + lane / nb) * kKeyGroup + lane % nb * br, br, key_lo, p.sinks, K,
                  tb.pg[0], tb.rw[0], bad);
         bad_page |= bad;
       } else {
@@ -1156,7 +1157,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!acquire(slot[it], mine[it])) return false;
           nmine += mine[it] ? 1 : 0;
         }
-        const bool tail_grp = seq_group<WINDOW>(ax, kTileGroups * tile + vp) == ngroups - 1 && tail_rows != 0;
+        const bool tail_grp = seq_group<SPAN>(ax, kTileGroups * tile + vp) == ngroups - 1 && tail_rows != 0;
         const bool tail = tail_grp && nmine != 0;
         // this CTA's 128-byte column blocks of V: bf16 blocks {0,1,4,5} or {2,3,6,7}
         // (two per slot, one slot per output chunk), e4m3 blocks {rank, 2 + rank}
@@ -1279,27 +1280,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 }  // namespace tc
 
-template <bool E4M3, bool ONE_BOX, bool WINDOW>
+template <bool E4M3, bool ONE_BOX, int SPAN>
 static cudaError_t launch_variant(const DecodeParams& p, const KvMaps& maps, cudaStream_t stream) {
   const dim3 grid(2 * p.num_clusters), block(tc::kThreads);
   const int smem = tc::smem_bytes<E4M3>();
   cudaError_t e =
-      cudaFuncSetAttribute(tc::split_kv_tc<E4M3, ONE_BOX, WINDOW>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      cudaFuncSetAttribute(tc::split_kv_tc<E4M3, ONE_BOX, SPAN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  tc::split_kv_tc<E4M3, ONE_BOX, WINDOW><<<grid, block, smem, stream>>>(p, maps);
+  tc::split_kv_tc<E4M3, ONE_BOX, SPAN><<<grid, block, smem, stream>>>(p, maps);
   return cudaGetLastError();
 }
 
-cudaError_t launch_split_kv(const DecodeParams& p, const KvMaps& maps, cudaStream_t stream) {
+template <int SPAN>
+static cudaError_t launch_span(const DecodeParams& p, const KvMaps& maps, cudaStream_t stream) {
   const bool one = p.page_size >= kKeyGroup;
-  if (p.window_left >= 0) {
-    if (p.qkv_e4m3)
-      return one ? launch_variant<true, true, true>(p, maps, stream) : launch_variant<true, false, true>(p, maps, stream);
-    return one ? launch_variant<false, true, true>(p, maps, stream) : launch_variant<false, false, true>(p, maps, stream);
-  }
-  if (p.qkv_e4m3)
-    return one ? launch_variant<true, true, false>(p, maps, stream) : launch_variant<true, false, false>(p, maps, stream);
-  return one ? launch_variant<false, true, false>(p, maps, stream) : launch_variant<false, false, false>(p, maps, stream);
+  if (p.qkv_e4m3) return one ? launch_variant<true, true, SPAN>(p, maps, stream) : launch_variant<true, false, SPAN>(p, maps, stream);
+  return one ? launch_variant<false, true, SPAN>(p, maps, stream) : launch_variant<false, false, SPAN>(p, maps, stream);
+}
+
+cudaError_t launch_split_kv(const DecodeParams& p, const KvMaps& maps, cudaStream_t stream) {
+  if (p.window_left < 0) return launch_span<kWhole>(p, maps, stream);
+  return p.sinks > 0 ? launch_span<kSinks>(p, maps, stream) : launch_span<kWindow>(p, maps, stream);
 }
 
 int split_kv_max_clusters(int device, bool e4m3) {
@@ -1322,12 +1323,12 @@ int split_kv_max_clusters(int device, bool e4m3) {
   cudaError_t e;
   if (e4m3) {
     cfg.dynamicSmemBytes = tc::smem_bytes<true>();
-    cudaFuncSetAttribute(tc::split_kv_tc<true, true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
-    e = cudaOccupancyMaxActiveClusters(&n, tc::split_kv_tc<true, true, false>, &cfg);
+    cudaFuncSetAttribute(tc::split_kv_tc<true, true, kWhole>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    e = cudaOccupancyMaxActiveClusters(&n, tc::split_kv_tc<true, true, kWhole>, &cfg);
   } else {
     cfg.dynamicSmemBytes = tc::smem_bytes<false>();
-    cudaFuncSetAttribute(tc::split_kv_tc<false, true, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
-    e = cudaOccupancyMaxActiveClusters(&n, tc::split_kv_tc<false, true, false>, &cfg);
+    cudaFuncSetAttribute(tc::split_kv_tc<false, true, kWhole>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes);
+    e = cudaOccupancyMaxActiveClusters(&n, tc::split_kv_tc<false, true, kWhole>, &cfg);
   }
   if (e == cudaSuccess && n > 0) return n;
   cudaGetLastError();

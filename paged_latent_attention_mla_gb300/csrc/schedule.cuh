@@ -90,32 +90,32 @@ struct SubSpan {
 };
 
 // span of sub-band k of request b, given the request's lengths
-template <bool WINDOW>
+template <int SPAN>
 __device__ __forceinline__ SubSpan sub_span(const DecodeParams& p, const DealShape& d, int b, int k, int K, int Kg) {
   const int i0 = k * d.wb, i1 = min(d.Qb, i0 + d.wb) - 1;
   int t0, t1;
   work_tokens(i0, i1, p.Sq, p.H, t0, t1);
-  const KeySpan s = window_span<WINDOW>(tokens_span(p, b, t0, t1, K, Kg), K);
+  const KeySpan s = window_span<SPAN>(tokens_span(p, b, t0, t1, K, Kg), K);
   SubSpan u;
   u.key_lo = s.lo;
   u.end = s.end;
-  u.axis = tile_axis<WINDOW>(s.lo, p.sinks);
-  tile_span<WINDOW>(s, u.axis, p.sinks, u.tile_lo, u.n);
+  u.axis = tile_axis<SPAN>(s.lo, p.sinks);
+  tile_span<SPAN>(s, u.axis, p.sinks, u.tile_lo, u.n);
   return u;
 }
 
 // span of work row i of request b on its sub-band's axis
-template <bool WINDOW>
+template <int SPAN>
 __device__ __forceinline__ void work_span(const DecodeParams& p, int b, int i, int K, int Kg, TileAxis axis, int& tlo,
                                           int& n) {
   int t0, t1;
   work_tokens(i, i, p.Sq, p.H, t0, t1);
-  tile_span<WINDOW>(window_span<WINDOW>(tokens_span(p, b, t0, t1, K, Kg), K), axis, p.sinks, tlo, n);
+  tile_span<SPAN>(window_span<SPAN>(tokens_span(p, b, t0, t1, K, Kg), K), axis, p.sinks, tlo, n);
 }
 
 // Block-wide: fills prefix[0..S] (prefix[S] = T) in shared memory.  scratch needs
 // S + 1 + 32 ints.  All threads of the block must call it.
-template <bool WINDOW>
+template <int SPAN>
 __device__ __forceinline__ Sched build_schedule(const DecodeParams& p, int32_t* scratch, uint32_t* err_flag) {
   const DealShape d = deal_shape(p.B, p.Sq, p.H, p.num_clusters);
   const int S = d.S;
@@ -129,7 +129,7 @@ __device__ __forceinline__ Sched build_schedule(const DecodeParams& p, int32_t* 
   for (int s = s0; s < s1; ++s) {
     const int b = s / d.nsub;
     const int K = clamp_len(p, b, s % d.nsub == 0 ? err_flag : nullptr);  // a bad length flagged once
-    const int U = sub_span<WINDOW>(p, d, b, s % d.nsub, K, global_len(p, b, K)).n;
+    const int U = sub_span<SPAN>(p, d, b, s % d.nsub, K, global_len(p, b, K)).n;
     const int cost = U > 0 ? p.piece_units + kUnitsPerTile * U : 0;
     prefix[s] = cost;
     local += cost;
@@ -198,7 +198,7 @@ __device__ __forceinline__ int row_parts(const Sched& sc, int pu, int s, int ulo
 // cluster's share (the spans of a super-row take one read of the request's lengths, and
 // the lanes read theirs together).  The first kSmemSegs go to `segs` in shared memory,
 // the rest to `overflow` (workspace).  Returns the number of pieces (in every lane).
-template <bool WINDOW>
+template <int SPAN>
 __device__ __forceinline__ int build_segments(const DecodeParams& p, const Sched& sc, int c, Segment* segs,
                                               Segment* overflow) {
   const DealShape& d = sc.d;
@@ -217,10 +217,10 @@ __device__ __forceinline__ int build_segments(const DecodeParams& p, const Sched
       const int b = s / d.nsub, k = s % d.nsub, i = k * d.wb + j;
       if (i < d.Qb) {
         const int K = clamp_len(p, b, nullptr), Kg = global_len(p, b, K);
-        const SubSpan sub = sub_span<WINDOW>(p, d, b, k, K, Kg);
+        const SubSpan sub = sub_span<SPAN>(p, d, b, k, K, Kg);
         const int ulo = sub.tile_lo, U = sub.n;
         int tlo, nt;
-        work_span<WINDOW>(p, b, i, K, Kg, sub.axis, tlo, nt);
+        work_span<SPAN>(p, b, i, K, Kg, sub.axis, tlo, nt);
         // the sub-band's tiles whose first unit lies in [cb, ce): i in [ceil((cb - pb) / 4),
         // ceil((ce - pb) / 4)), pb the unit of its tile 0; then those of this work row
         const long long pb = tile_unit(sc.prefix[s], p.piece_units, 0);
@@ -255,7 +255,7 @@ __device__ __forceinline__ int build_segments(const DecodeParams& p, const Sched
 
 // Row table for the reduction and the header: the work rows spread over every CTA of
 // the split-KV kernel, the header from block 0.
-template <bool WINDOW>
+template <int SPAN>
 __device__ __forceinline__ void write_row_table(const DecodeParams& p, const Sched& sc) {
   const DealShape& d = sc.d;
   const WsLayout L = ws_layout(p.B, p.Sq, p.H, p.num_clusters, p.partial_f16);
@@ -264,9 +264,9 @@ __device__ __forceinline__ void write_row_table(const DecodeParams& p, const Sch
     const int b = w / d.Qb, i = w % d.Qb;
     const int k = i / d.wb, j = i % d.wb, s = b * d.nsub + k;
     const int K = clamp_len(p, b, nullptr), Kg = global_len(p, b, K);
-    const SubSpan sub = sub_span<WINDOW>(p, d, b, k, K, Kg);
+    const SubSpan sub = sub_span<SPAN>(p, d, b, k, K, Kg);
     int tlo, n;
-    work_span<WINDOW>(p, b, i, K, Kg, sub.axis, tlo, n);
+    work_span<SPAN>(p, b, i, K, Kg, sub.axis, tlo, n);
     RowInfo ri;
     ri.tile_lo = tlo;
     ri.n_tiles = n;

@@ -49,13 +49,13 @@ __device__ __forceinline__ void zero_block_rows(uint8_t* block, int row0, int la
 // Page id and row offset of the box of keys [key0, key0 + rows) of request b (K keys),
 // P = 1 << page_shift: no key below K, with a window none at key_lo or later nor below sinks
 // (the pages between may have been given up: they are not even looked up), or an invalid page
-// id -> page num_pages (zero fill), bad set for the last.  Branch-free after the load, so a caller that reads ahead
-// does not wait for the page table until it uses the page.
-template <bool WINDOW>
+// id -> page num_pages (zero fill), bad set for the last.  Branch-free after the load, so a
+// caller that reads ahead does not wait for the page table until it uses the page.
+template <int SPAN>
 __device__ __forceinline__ void box_page(const int32_t* page_table, int pt_stride, int num_pages, int page_shift, int b,
                                          int key0, int rows, int key_lo, int sinks, int K, int& page, int& row,
                                          bool& bad) {
-  const bool in = key0 < K && (!WINDOW || key0 + rows > key_lo || key0 < sinks);
+  const bool in = key0 < K && (SPAN == kWhole || key0 + rows > key_lo || (SPAN == kSinks && key0 < sinks));
   const int lp = key0 >> page_shift;
   const int v = in ? __ldg(page_table + (size_t)b * pt_stride + lp) : num_pages;
   bad = in && (unsigned)v >= (unsigned)num_pages;
