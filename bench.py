@@ -49,10 +49,10 @@ ALL = ["uniform", "varlen", "fp8spec", "window"]
 # the kernel sources it was taken on: reported when their hash still matches, else null.
 KERNEL_SOURCES = ("mla_split_tc.cu", "mla_common.cuh", "schedule.cuh", "tma_pages.cuh", "ptx.cuh")
 NCU_TRAFFIC = {
-    "uniform": {"sources_sha256": "ef9310493dc0d3536f2f08ff5270e1de64699ab9b8c7488f93f813e68fe41665", "bytes": 322583296 + 7560704},
-    "varlen": {"sources_sha256": "ef9310493dc0d3536f2f08ff5270e1de64699ab9b8c7488f93f813e68fe41665", "bytes": 558726656 + 15559424},
-    "fp8spec": {"sources_sha256": "ef9310493dc0d3536f2f08ff5270e1de64699ab9b8c7488f93f813e68fe41665", "bytes": 310206976 + 8817152},
-    "window": {"sources_sha256": "ef9310493dc0d3536f2f08ff5270e1de64699ab9b8c7488f93f813e68fe41665", "bytes": 43287552 + 655104},
+    "uniform": {"sources_sha256": "4cb85a36b0da50269a3185e717808cd1b0a9cdbef1e3e064d025f64357ce8dda", "bytes": 322647296 + 8256256},
+    "varlen": {"sources_sha256": "4cb85a36b0da50269a3185e717808cd1b0a9cdbef1e3e064d025f64357ce8dda", "bytes": 558186496 + 15566848},
+    "fp8spec": {"sources_sha256": "4cb85a36b0da50269a3185e717808cd1b0a9cdbef1e3e064d025f64357ce8dda", "bytes": 310216192 + 8865280},
+    "window": {"sources_sha256": "4cb85a36b0da50269a3185e717808cd1b0a9cdbef1e3e064d025f64357ce8dda", "bytes": 43281664 + 628224},
 }
 
 
